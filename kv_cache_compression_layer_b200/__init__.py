@@ -1,5 +1,5 @@
-"""Python binding of libkvcomp.so (the C ABI declared in include/kvcomp.h and
-include/kvcomp_next.h).
+"""Python binding of libkvcomp.so (the C ABI declared in include/kvcomp.h,
+include/kvcomp_next.h and include/kvcomp_paged.h).
 
 Argument marshalling only: every step of the path runs in the library's
 sm_100a kernels. Functions take torch tensors (or raw device addresses as
@@ -23,8 +23,10 @@ LIB_PATH = os.path.join(HERE, "libkvcomp_debug.so" if DEBUG_CHECKS else "libkvco
 
 KV_OK, KV_ERR_ARG, KV_ERR_UNSUPPORTED_L, KV_ERR_BUDGET, KV_ERR_WORKSPACE, KV_ERR_CUDA, KV_ERR_TIMEOUT = range(7)
 KV_DEV_TIMEOUT, KV_DEV_BUDGET, KV_DEV_CAPACITY, KV_DEV_RANGE, KV_DEV_BOUNDS = 0x1, 0x2, 0x4, 0x8, 0x10
+KV_DEV_PAGES, KV_DEV_BUSY = 0x20, 0x40
 KV_F32, KV_BF16 = 0, 1
 KV_MAX_SEQ = 64
+KV_PAGED_MAX_QUERIES = 64
 META_INTS = 8
 
 # Every symbol the headers under include/ declare.
@@ -33,7 +35,9 @@ EXPORTS = ("kv_rows", "kv_check_lengths", "kv_workspace_bytes", "kv_total_slots"
            "kv_status_string", "kv_score_noalloc", "kv_decode_scratch_bytes", "kv_allocate_global",
            "kv_select_gather_segmented", "kv_voxzip_pool", "kv_wnw_chunk_count", "kv_wnw_state_ints",
            "kv_wnw_init", "kv_wnw_update", "kv_wnw_recall", "kv_c3_index_layout", "kv_c3_build", "kv_c3_step",
-           "kv_set_wait_limit_ns", "kv_score_noalloc_status", "kv_debug_checks", "kv_debug_check_word")
+           "kv_set_wait_limit_ns", "kv_score_noalloc_status", "kv_debug_checks", "kv_debug_check_word",
+           "kv_select", "kv_paged_page_bytes", "kv_paged_ws_bytes", "kv_paged_rebuild", "kv_paged_append",
+           "kv_paged_load", "kv_paged_attn", "kv_paged_fork", "kv_paged_copy", "kv_paged_compact", "kv_paged_free")
 KV_NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -68,6 +72,16 @@ class kv_cache(C.Structure):
                 ("total_slots", C.c_int64), ("scratch", C.c_void_p), ("scratch_bytes", C.c_size_t)]
 
 
+class kv_paged_shape(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n_seqs", "n_layers", "n_kv_heads", "group", "head_dim", "dtype", "n_pages",
+                                         "max_pages", "quant_group", "page_tokens")]
+
+
+class kv_paged_cache(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("table", C.c_void_p), ("len", C.c_void_p), ("ref", C.c_void_p),
+                ("free_bits", C.c_void_p), ("status", C.c_void_p), ("ws", C.c_void_p), ("ws_bytes", C.c_size_t)]
+
+
 class KvError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn} failed: {status_string(status)} ({status})")
@@ -89,6 +103,7 @@ def lib():
         Ps, Pp, Pc = C.POINTER(kv_shape), C.POINTER(kv_params), C.POINTER(kv_cache)
         Pw = C.POINTER(kv_wnw_params)
         Pc3, Pl3 = C.POINTER(kv_c3_params), C.POINTER(kv_c3_layout)
+        Pps, Ppc = C.POINTER(kv_paged_shape), C.POINTER(kv_paged_cache)
         sig = {
             "kv_rows": (I64, [Ps, I32]),
             "kv_check_lengths": (C.c_int, [Ps, P, I32]),
@@ -119,6 +134,17 @@ def lib():
             "kv_c3_index_layout": (C.c_int, [Ps, P, I32, Pc3, Pl3]),
             "kv_c3_build": (C.c_int, [Ps, P, I32, Pc3, P, P, P]),
             "kv_c3_step": (C.c_int, [Ps, P, I32, Pc3, P, P, P, P, P, P]),
+            "kv_select": (C.c_int, [Ps, P, I32, P, P, P, P, P]),
+            "kv_paged_page_bytes": (SZ, [Pps]),
+            "kv_paged_ws_bytes": (SZ, [Pps]),
+            "kv_paged_rebuild": (C.c_int, [Pps, Ppc, P]),
+            "kv_paged_append": (C.c_int, [Pps, Ppc, P, I32, I32, I32, P, P, I64, I32, P, P, P, P, P]),
+            "kv_paged_load": (C.c_int, [Pps, Ppc, P, I32, I32, I32, P, I64, P, P, P]),
+            "kv_paged_attn": (C.c_int, [Pps, Ppc, P, I32, I32, I32, I32, P, P, P, P]),
+            "kv_paged_fork": (C.c_int, [Pps, Ppc, P, P, I32, P]),
+            "kv_paged_copy": (C.c_int, [Pps, Ppc, P, Pps, Ppc, P, I32, P]),
+            "kv_paged_compact": (C.c_int, [Pps, Ppc, P, P, I32, P, P, P, P]),
+            "kv_paged_free": (C.c_int, [Pps, Ppc, P, I32, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -367,6 +393,92 @@ def kv_c3_step(shape, L, p, K, V, q, index, out, stream=None):
                                           _ptr(index), _ptr(out), _stream(stream)))
 
 
+def kv_select(shape, L, s_hat, b, slot_off, idx, stream=None):
+    arr, n = _L(L)
+    _check("kv_select", lib().kv_select(C.byref(shape), arr, n, _ptr(s_hat), _ptr(b), _ptr(slot_off), _ptr(idx),
+                                        _stream(stream)))
+
+
+def make_paged_shape(n_seqs: int, n_layers: int, n_kv_heads: int, group: int, head_dim: int, dtype: int,
+                     n_pages: int, max_pages: int, quant_group: int = 64, page_tokens: int = 64) -> kv_paged_shape:
+    return kv_paged_shape(n_seqs, n_layers, n_kv_heads, group, head_dim, dtype, n_pages, max_pages, quant_group,
+                          page_tokens)
+
+
+def make_paged_cache(pages, table, lens, ref, free_bits, status, ws, ws_bytes: Optional[int] = None) -> kv_paged_cache:
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
+    return kv_paged_cache(_ptr(pages), _ptr(table), _ptr(lens), _ptr(ref), _ptr(free_bits), _ptr(status), _ptr(ws),
+                          int(ws_bytes))
+
+
+def kv_paged_page_bytes(shape: kv_paged_shape) -> int:
+    return lib().kv_paged_page_bytes(C.byref(shape))
+
+
+def kv_paged_ws_bytes(shape: kv_paged_shape) -> int:
+    return lib().kv_paged_ws_bytes(C.byref(shape))
+
+
+def kv_paged_rebuild(shape, cache: kv_paged_cache, stream=None):
+    _check("kv_paged_rebuild", lib().kv_paged_rebuild(C.byref(shape), C.byref(cache), _stream(stream)))
+
+
+def kv_paged_append(shape, cache, seqs, K, V, n_src: int, n_each: int = 0, count=None, src_off=None, idx=None,
+                    idx_off=None, layer0: int = 0, n_lay: Optional[int] = None, stream=None):
+    arr, n = _L(seqs)
+    _check("kv_paged_append",
+           lib().kv_paged_append(C.byref(shape), C.byref(cache), arr, n, layer0,
+                                 shape.n_layers - layer0 if n_lay is None else n_lay, _ptr(K), _ptr(V), n_src, n_each,
+                                 _ptr(count), _ptr(src_off), _ptr(idx), _ptr(idx_off), _stream(stream)))
+
+
+def kv_paged_load(shape, cache, seqs, out_off, n_out: int, K_out, V_out, layer0: int = 0,
+                  n_lay: Optional[int] = None, stream=None):
+    arr, n = _L(seqs)
+    _check("kv_paged_load",
+           lib().kv_paged_load(C.byref(shape), C.byref(cache), arr, n, layer0,
+                               shape.n_layers - layer0 if n_lay is None else n_lay, _ptr(out_off), n_out, _ptr(K_out),
+                               _ptr(V_out), _stream(stream)))
+
+
+def kv_paged_attn(shape, cache, seqs, q, out, lse=None, n_q: int = 1, layer0: int = 0, n_lay: Optional[int] = None,
+                  stream=None):
+    arr, n = _L(seqs)
+    _check("kv_paged_attn",
+           lib().kv_paged_attn(C.byref(shape), C.byref(cache), arr, n, layer0,
+                               shape.n_layers - layer0 if n_lay is None else n_lay, n_q, _ptr(q), _ptr(out),
+                               _ptr(lse), _stream(stream)))
+
+
+def _pairs(src, dst):
+    if len(src) != len(dst):
+        raise ValueError("src and dst name a different number of sequences")
+    return _L(src)[0], _L(dst)[0], len(src)
+
+
+def kv_paged_fork(shape, cache, src, dst, stream=None):
+    a, b, n = _pairs(src, dst)
+    _check("kv_paged_fork", lib().kv_paged_fork(C.byref(shape), C.byref(cache), a, b, n, _stream(stream)))
+
+
+def kv_paged_copy(src_shape, src_cache, src, dst_shape, dst_cache, dst, stream=None):
+    a, b, n = _pairs(src, dst)
+    _check("kv_paged_copy", lib().kv_paged_copy(C.byref(src_shape), C.byref(src_cache), a, C.byref(dst_shape),
+                                                C.byref(dst_cache), b, n, _stream(stream)))
+
+
+def kv_paged_compact(shape, cache, src, dst, idx, idx_off, count, stream=None):
+    a, b, n = _pairs(src, dst)
+    _check("kv_paged_compact", lib().kv_paged_compact(C.byref(shape), C.byref(cache), a, b, n, _ptr(idx),
+                                                      _ptr(idx_off), _ptr(count), _stream(stream)))
+
+
+def kv_paged_free(shape, cache, seqs, stream=None):
+    arr, n = _L(seqs)
+    _check("kv_paged_free", lib().kv_paged_free(C.byref(shape), C.byref(cache), arr, n, _stream(stream)))
+
+
 def kv_read_device_status(status_dev, stream=None) -> int:
     host = C.c_int32(0)
     _check("kv_read_device_status", lib().kv_read_device_status(_ptr(status_dev), C.byref(host), _stream(stream)))
@@ -386,7 +498,8 @@ def kv_debug_check_word(clear: bool = False) -> int:
     return host.value
 
 
-from .pipeline import Compressor  # noqa: E402  (the torch-side convenience wrapper)
+from .paged import PagedCache  # noqa: E402  (the torch-side convenience wrappers)
+from .pipeline import Compressor  # noqa: E402
 
 __all__ = ["kv_shape", "kv_params", "kv_cache", "KvError", "lib", "make_shape", "make_params", "make_cache",
            "kv_rows", "kv_check_lengths", "kv_workspace_bytes", "kv_total_slots", "kv_score", "kv_score_noalloc",
@@ -397,4 +510,7 @@ __all__ = ["kv_shape", "kv_params", "kv_cache", "KvError", "lib", "make_shape", 
            "pack_segments", "ASR_SEGMENT_BYTES", "kv_wnw_params", "make_wnw_params", "kv_wnw_chunk_count",
            "kv_wnw_state_ints", "kv_wnw_init", "kv_wnw_update", "kv_wnw_recall", "kv_c3_params", "kv_c3_layout",
            "make_c3_params", "kv_c3_index_layout", "kv_c3_build", "kv_c3_step", "status_string",
-           "Compressor", "EXPORTS", "KV_F32", "KV_BF16", "META_INTS"]
+           "kv_select", "kv_paged_shape", "kv_paged_cache", "make_paged_shape", "make_paged_cache",
+           "kv_paged_page_bytes", "kv_paged_ws_bytes", "kv_paged_rebuild", "kv_paged_append", "kv_paged_load",
+           "kv_paged_attn", "kv_paged_fork", "kv_paged_copy", "kv_paged_compact", "kv_paged_free", "PagedCache",
+           "KV_DEV_PAGES", "KV_DEV_BUSY", "KV_PAGED_MAX_QUERIES", "Compressor", "EXPORTS", "KV_F32", "KV_BF16", "META_INTS"]

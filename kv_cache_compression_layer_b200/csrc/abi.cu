@@ -8,6 +8,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "../../include/kvcomp_paged.h"
 #include "internal.h"
 
 namespace kvc {
@@ -91,7 +92,7 @@ static bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(
 
 // Host-side fault injection for tests: KV_FAULT_INJECT=<entry point name>
 // makes that entry point fail with KV_ERR_CUDA before launching anything.
-static bool fault_injected(const char* name) {
+bool fault_injected(const char* name) {
   const char* v = std::getenv("KV_FAULT_INJECT");
   return v && std::strcmp(v, name) == 0;
 }
@@ -263,6 +264,18 @@ int kv_select_gather_segmented(const kv_shape* shape, const int32_t* L, int32_t 
   if (!K || !V) return KV_ERR_ARG;
   return launch_select_gather(*shape, m, s_hat, K, V, b, slot_off, idx, Kc, Vc, n_segments,
                               static_cast<cudaStream_t>(stream));
+}
+
+int kv_select(const kv_shape* shape, const int32_t* L, int32_t n_seq, const float* s_hat, const int32_t* b,
+              const int64_t* slot_off, int32_t* idx, void* stream) {
+  if (fault_injected("kv_select")) return KV_ERR_CUDA;
+  if (!shape_ok(shape)) return KV_ERR_ARG;
+  RowMap m;
+  int st = make_row_map(*shape, L, n_seq, m);
+  if (st) return st;
+  for (const void* p : {(const void*)s_hat, (const void*)b, (const void*)slot_off, (const void*)idx})
+    if (!aligned16(p)) return KV_ERR_ARG;
+  return launch_select(*shape, m, s_hat, b, slot_off, idx, 0, static_cast<cudaStream_t>(stream));
 }
 
 static bool cache_ok(const kv_cache* c) {

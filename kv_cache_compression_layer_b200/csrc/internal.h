@@ -31,6 +31,8 @@ int launch_sss(const RowMap& m, const float* s, float* s_hat, int32_t* kstar, fl
                cudaStream_t st);
 int launch_allocate(const kv_shape& sh, const RowMap& m, const kv_params& p, const float* S, int32_t* b,
                     int64_t* slot_off, bool global, cudaStream_t st);
+int launch_select(const kv_shape& sh, const RowMap& m, const float* s_hat, const int32_t* b,
+                  const int64_t* slot_off, int32_t* idx, int nseg, cudaStream_t st);
 int launch_select_gather(const kv_shape& sh, const RowMap& m, const float* s_hat, const void* K, const void* V,
                          const int32_t* b, const int64_t* slot_off, int32_t* idx, void* Kc, void* Vc, int nseg,
                          cudaStream_t st);
@@ -46,6 +48,9 @@ int launch_decode(const kv_shape& sh, const RowMap& m, const kv_params& p, const
 // launches, and wait_limit_ns() is the value a launch passes to its kernels.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 unsigned long long wait_limit_ns();
+
+// Host-side fault injection for tests (KV_FAULT_INJECT names this entry point).
+bool fault_injected(const char* name);
 
 inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? KV_OK : KV_ERR_CUDA; }
 

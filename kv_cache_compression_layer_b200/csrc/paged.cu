@@ -1,0 +1,1123 @@
+// The paged 4-bit KV cache: storing tokens (quantisation), reading them back,
+// and forking, copying, compacting and freeing pages. Declarations and the
+// formats are in include/kvcomp_paged.h; attention is in paged_attn.cu.
+//
+// A call that needs pages runs a plan kernel (one CTA) and a data kernel.
+// The plan sums the rows' needs in call-row order, lists that many of the
+// lowest free pages from the bitmap and refuses the rows that do not fit; the
+// data kernel moves the tokens and, where it reaches the first token of a new
+// page, enters the page into the row's list, its count and the bitmap. No
+// device wait, no atomics whose order shows: a page's count is an integer sum
+// and the bitmap a set.
+#include <climits>
+
+#include "paged_common.cuh"
+
+namespace kvc {
+
+bool paged_shape_ok(const kv_paged_shape* sh) {
+  if (!sh) return false;
+  if (sh->n_seqs < 1 || sh->n_layers < 1 || sh->n_kv_heads < 1 || sh->group < 1 || sh->group > 16) return false;
+  if (sh->n_seqs > KV_PAGED_MAX_ROWS || sh->n_layers > KV_PAGED_MAX_ROWS || sh->n_kv_heads > KV_PAGED_MAX_ROWS)
+    return false;
+  if ((long long)sh->n_layers * sh->n_kv_heads > KV_PAGED_MAX_ROWS) return false;
+  if ((long long)sh->n_seqs * sh->n_layers * sh->n_kv_heads > KV_PAGED_MAX_ROWS) return false;
+  if (sh->head_dim != 64 && sh->head_dim != 128) return false;
+  if (sh->dtype != KV_BF16 && sh->dtype != KV_F32) return false;
+  if (sh->quant_group != 32 && sh->quant_group != 64 && sh->quant_group != 128) return false;
+  if (sh->quant_group > sh->head_dim) return false;
+  if (sh->page_tokens != 16 && sh->page_tokens != 32 && sh->page_tokens != 64 && sh->page_tokens != 128) return false;
+  if (sh->n_pages < 1 || sh->n_pages > KV_PAGED_MAX_PAGES) return false;
+  if (sh->max_pages < 1 || (long long)sh->max_pages * sh->page_tokens > KV_PAGED_MAX_TOKENS) return false;
+  return true;
+}
+
+PageGeom page_geom(const kv_paged_shape& sh) {
+  PageGeom g;
+  g.P = sh.page_tokens;
+  g.log_p = sh.page_tokens == 16 ? 4 : sh.page_tokens == 32 ? 5 : sh.page_tokens == 64 ? 6 : 7;
+  g.d = sh.head_dim;
+  g.qg = sh.quant_group;
+  g.G = sh.head_dim / sh.quant_group;
+  g.v = g.P * g.d / 2;
+  g.ks = 2 * g.v;
+  g.vs = g.ks + g.P * g.G * 4;
+  g.bytes = g.vs + g.P * g.G * 4;
+  g.n_pages = sh.n_pages;
+  g.max_pages = sh.max_pages;
+  return g;
+}
+
+static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+PagedWs paged_ws_layout(const kv_paged_shape& sh) {
+  const size_t rows = (size_t)(sh.n_seqs < KV_MAX_SEQ ? sh.n_seqs : KV_MAX_SEQ) * sh.n_layers * sh.n_kv_heads;
+  PagedWs w;
+  w.plan = 0;
+  w.unit = align256(w.plan + rows * sizeof(RowPlan));
+  w.take = align256(w.unit + (rows + 1) * sizeof(int));
+  w.att_base = align256(w.take + (size_t)sh.n_pages * sizeof(int));
+  w.part = align256(w.att_base + (size_t)sm_count() * kAttnCtasPerSm * 4 * sizeof(int));
+  // two partials per attention CTA: (max, sum) and the output of up to kAttnQ query rows
+  w.bytes = align256(w.part + (size_t)sm_count() * kAttnCtasPerSm * 2 * kAttnQ * (sh.head_dim + 2) * sizeof(float));
+  return w;
+}
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+enum PlanOp { kAppend, kFork, kCopy, kCompact };
+
+struct PlanArgs {
+  PageGeom g;         // of the cache that takes pages
+  SeqRows dst, src;   // src: fork, copy, compact
+  PagedCache c;       // the cache that takes pages
+  const int32_t* src_len;
+  int src_max;        // tokens a source row can hold at most
+  const int32_t* count;
+  int n_each;
+  RowPlan* plan;
+  int* unit;  // [rows + 1] units of kUnit tokens before each row (append, compact)
+  int* take;
+};
+
+// Exclusive sum over the block in thread order; *total = the block's sum.
+__device__ long long block_excl(long long v, long long* total, long long* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    long long t = sh[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += y;
+    }
+    sh[32 + lane] = t;
+  }
+  __syncthreads();
+  *total = sh[63];
+  return x - v + (warp ? sh[32 + warp - 1] : 0);
+}
+
+__device__ __forceinline__ int pages_of(const PageGeom& g, int tokens) { return (tokens + g.P - 1) >> g.log_p; }
+
+template <int OP>
+__global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanArgs a) {
+  __shared__ long long sh[64];
+  const PageGeom& g = a.g;
+  const int row_max = g.max_pages << g.log_p;  // tokens a row can hold
+  pdl_launch_dependents();
+  pdl_wait();
+  int bad = 0;
+  // needs of the rows, in order
+  long long demand = 0;
+  for (int i0 = 0; i0 < a.dst.n_rows; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    RowPlan p{0, -1, 0, 0};
+    int need = 0;
+    if (i < a.dst.n_rows) {
+      const int tr = table_row(a.dst, i);
+      const int held = a.c.len[tr];
+      bool ok = held >= 0 && held <= row_max;
+      if (!ok) bad |= KV_DEV_BOUNDS;
+      if (OP == kAppend) {
+        const int n = a.count ? max(0, a.count[i]) : a.n_each;
+        p.old = held;
+        p.n = n;
+        if (ok && n > row_max - held) {
+          ok = false;
+          bad |= KV_DEV_CAPACITY;
+        }
+        if (ok) {
+          p.fresh = pages_of(g, held);
+          need = pages_of(g, held + n) - p.fresh;
+        }
+      } else {
+        const int ts = table_row(a.src, i);
+        const int sl = a.src_len[ts];
+        if (sl < 0 || sl > a.src_max) {
+          ok = false;
+          bad |= KV_DEV_BOUNDS;
+        }
+        const bool in_place = OP == kCompact && ts == tr;
+        if (ok && held != 0 && !in_place) {
+          ok = false;
+          bad |= KV_DEV_BUSY;
+        }
+        p.old = sl;
+        p.n = OP == kCompact ? max(0, a.count[i]) : sl;
+        if (ok && p.n > row_max) {
+          ok = false;
+          bad |= KV_DEV_CAPACITY;
+        }
+        if (ok) {
+          p.fresh = OP == kFork ? p.n >> g.log_p : 0;
+          need = pages_of(g, p.n) - p.fresh;
+        }
+      }
+    }
+    long long tot;
+    const long long at = demand + block_excl(need, &tot, sh);
+    if (i < a.dst.n_rows) {
+      p.take = need == 0 ? 0 : (int)(at < INT_MAX ? at : INT_MAX);
+      a.plan[i] = p;
+    }
+    demand += tot;
+  }
+  // the lowest `demand` free pages (or all of them), a word of the bitmap per thread
+  long long found = 0;
+  const int words = (g.n_pages + 31) >> 5;
+  const int lane = threadIdx.x & 31;
+  for (int w0 = 0; w0 < words && found < demand; w0 += kPlanThreads) {
+    const int w = w0 + threadIdx.x;
+    const uint32_t bits = w < words ? a.c.free_bits[w] : 0u;
+    long long tot;
+    const long long at = found + block_excl(__popc(bits), &tot, sh);
+    for (int l = 0; l < 32; ++l) {  // the warp writes one lane's pages at a time
+      const uint32_t b = __shfl_sync(0xffffffffu, bits, l);
+      const long long r = __shfl_sync(0xffffffffu, at, l);
+      if (r >= demand) break;
+      const int rank = (int)r + __popc(b & ((1u << lane) - 1u));
+      const int page = ((w - lane + l) << 5) + lane;
+      if ((b >> lane) & 1u) {
+        if (rank < demand && page < g.n_pages) a.take[rank] = page;
+      }
+    }
+    found += tot;
+  }
+  // units of the rows that are served; lengths as they will be
+  long long units = 0;
+  for (int i0 = 0; i0 < a.dst.n_rows; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    int u = 0;
+    if (i < a.dst.n_rows) {
+      RowPlan p = a.plan[i];
+      if (p.fresh >= 0) {
+        const int end = OP == kAppend ? p.old + p.n : p.n;
+        const int need = pages_of(g, end) - p.fresh;
+        if (need > 0 && (long long)p.take + need > found) {
+          bad |= KV_DEV_PAGES;
+          a.plan[i].fresh = -1;
+        } else {
+          a.c.len[table_row(a.dst, i)] = end;
+          if (p.n > 0) u = OP == kAppend ? ((end + kUnit - 1) / kUnit - p.old / kUnit) : (end + kUnit - 1) / kUnit;
+        }
+      }
+    }
+    if (OP == kAppend || OP == kCompact) {
+      long long tot;
+      const long long at = units + block_excl(u, &tot, sh);
+      if (i < a.dst.n_rows) a.unit[i] = (int)at;
+      units += tot;
+    }
+  }
+  if ((OP == kAppend || OP == kCompact) && threadIdx.x == 0) a.unit[a.dst.n_rows] = (int)units;
+  if (bad) atomicOr(a.c.status, bad);
+}
+
+// Enters new page `page` as entry j of a row's list.
+__device__ __forceinline__ void claim_page(const PagedCache& c, const PageGeom& g, int trow, int j, int page) {
+  c.table[(size_t)trow * g.max_pages + j] = page;
+  c.ref[page] = 1;
+  atomicAnd(&c.free_bits[page >> 5], ~(1u << (page & 31)));
+}
+
+// Gives up one holder of a page.
+__device__ __forceinline__ void drop_page(const PagedCache& c, const PageGeom& g, int page) {
+  if (page < 0 || page >= g.n_pages) {
+    atomicOr(c.status, KV_DEV_BOUNDS);
+    return;
+  }
+  const int before = atomicSub(&c.ref[page], 1);
+  if (before == 1) atomicOr(&c.free_bits[page >> 5], 1u << (page & 31));
+  if (before < 1) {  // it had no holder: leave it free
+    atomicAdd(&c.ref[page], 1);
+    atomicOr(c.status, KV_DEV_BOUNDS);
+  }
+}
+
+// The row that unit u lies in (unit[row] <= u < unit[row + 1]), by the whole
+// warp: 32 probes a round. u < unit[n].
+__device__ __forceinline__ int find_unit_row(const int* unit, int n, int u) {
+  int lo = 0, hi = n;  // unit[lo] <= u, u < unit[hi]
+  const int lane = threadIdx.x & 31;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const bool le = at < hi && unit[at] <= u;
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    const int last = 31 - __clz(m);  // lane 0 always holds
+    const int nlo = lo + last * step;
+    hi = min(hi, nlo + step);
+    lo = nlo;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------- storing
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ uint32_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+
+// The code of x by its definition, in float64: the quotient's rounding does
+// not reach a half (x, m and s have at most 24, 8 and 8 bits).
+__device__ __noinline__ uint32_t code_exact(float x, float m, float s) {
+  const double q = ((double)x - (double)m) / (double)s;
+  return (uint32_t)rint(fmin(fmax(q, 0.0), 15.0));
+}
+
+// Quantises the 8 channels that a lane holds of a group spread over LG
+// consecutive lanes: the codes, channel n in bits 4 n; *scale the packed (s, m).
+// The float32 products are off by a few of their last bits, so where that
+// could tip a rounding (a step next to the middle of two bf16, a quotient
+// within 1e-5 of a half) the decision is made again in float64.
+template <int LG>
+__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t* scale) {
+  float mx = x[0], mn = x[0];
+#pragma unroll
+  for (int n = 1; n < 8; ++n) {
+    mx = max_nan(mx, x[n]);
+    mn = min_nan(mn, x[n]);
+  }
+#pragma unroll
+  for (int o = 1; o < LG; o <<= 1) {
+    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+  }
+  const float m = bf16_round(mn);
+  if (!(fabsf(mx) < INFINITY && fabsf(mn) < INFINITY && fabsf(m) < INFINITY)) {
+    *scale = 0x7fff7fffu;  // (NaN, NaN)
+    return 0u;
+  }
+  float s = 0.f;
+  if (mx > m) {
+    float f = __fmul_rn(__fsub_rn(mx, m), 1.f / 15.f);
+    const uint32_t low = __float_as_uint(f) & 0xffffu;
+    if (low - 0x7fe0u <= 0x40u || !(f > 1e-30f) || !(f < 1e37f)) f = (float)(((double)mx - (double)m) / 15.0);
+    s = bf16_round(f);
+  }
+  *scale = bf16_bits(s) | (bf16_bits(m) << 16);
+  if (s == 0.f) return 0u;
+  uint32_t w = 0;
+  float dev = 1.f;
+  if (s > 1e-30f) {
+    const float magic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits of the sum
+    const float r = __frcp_rn(s);
+    dev = 0.f;
+#pragma unroll
+    for (int n = 7; n >= 0; --n) {
+      const float q = fmaxf(__fmul_rn(__fsub_rn(x[n], m), r), 0.f);
+      const float y = __fadd_rn(q, magic);
+      dev = fmaxf(dev, fabsf(__fsub_rn(q, __fsub_rn(y, magic))));
+      w = (w << 4) + __float_as_uint(y);
+    }
+    w -= 0x3F400000u;  // what the eight shifted exponents of `magic` (0x4B400000) add up to
+  }
+  if (dev > 0.49999f) {
+    w = 0;
+#pragma unroll
+    for (int n = 7; n >= 0; --n) w = (w << 4) | code_exact(x[n], m, s);
+  }
+  return w;
+}
+
+// The same 8 channels back: m + c s, one rounding in float32.
+__device__ __forceinline__ void dequantise8(uint32_t w, uint32_t scale, float (&x)[8]) {
+  const float s = __uint_as_float(scale << 16), m = __uint_as_float(scale & 0xffff0000u);
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const float c = __uint_as_float(0x4B000000u | ((w >> (4 * n)) & 15u)) - 8388608.f;  // exact
+    x[n] = fmaf(c, s, m);
+  }
+}
+
+// 8 channels of a row, 16-byte loads and stores.
+template <bool F32>
+struct Row8;
+template <>
+struct Row8<false> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void* base, long long row, int d, int l) {
+    u = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + row * d)[l];
+  }
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(v[i] << 16);
+      x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void store(void* base, long long row, int d, int l, const float (&x)[8]) {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      v[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + row * d)[l] = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+};
+template <>
+struct Row8<true> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* base, long long row, int d, int l) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + row * d) + 2 * l;
+    a = p[0];
+    b = p[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(void* base, long long row, int d, int l, const float (&x)[8]) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + row * d) + 2 * l;
+    p[0] = make_float4(x[0], x[1], x[2], x[3]);
+    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+
+constexpr int kMoveWarps = 8;
+
+struct StoreArgs {
+  PageGeom g;
+  SeqRows rows;
+  PagedCache c;
+  const void* K;
+  const void* V;
+  long long n_src;
+  int n_each;
+  const int64_t* src_off;
+  const int32_t* idx;
+  const int64_t* idx_off;
+  const RowPlan* plan;
+  const int* unit;
+  const int* take;
+};
+
+// Warps take runs of units of 16 tokens (a unit starts at a multiple of 16 of
+// the row's tokens, so it lies in one page). D / 8 lanes hold a token's row, 8
+// channels each; a unit is quantised into shared memory in the page's layout
+// and written with 16-byte stores (each of its four parts is contiguous).
+template <int D, int QG, bool F32>
+__global__ void __launch_bounds__(kMoveWarps * 32) paged_store_kernel(const StoreArgs a) {
+  constexpr int G = D / QG, LT = D / 8, TPI = 32 / LT, ITER = kUnit / TPI, W = D / 32;
+  constexpr int kCode = kUnit * D / 2, kScale = kUnit * G * 4;
+  __shared__ __align__(16) uint8_t stage[kMoveWarps][2 * (kCode + kScale)];
+  const PageGeom& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int l = lane % LT, sub = lane / LT;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int n_rows = a.rows.n_rows;
+  const int total = a.unit[n_rows];
+  const long long nw = (long long)gridDim.x * kMoveWarps, w = (long long)blockIdx.x * kMoveWarps + warp;
+  const int u0 = (int)(w * total / nw), u1 = (int)((w + 1) * total / nw);
+  if (u0 >= u1) return;
+  uint8_t* st = stage[warp];
+  int row = find_unit_row(a.unit, n_rows, u0);
+  int bad = 0;
+  for (int u = u0; u < u1; ++u) {
+    if (u >= a.unit[row + 1]) row = find_unit_row(a.unit, n_rows, u);
+    const RowPlan p = a.plan[row];
+    const int trow = table_row(a.rows, row);
+    const int pos0 = (p.old / kUnit + u - a.unit[row]) * kUnit;     // first token of the unit
+    const int t0 = max(pos0, p.old), t1 = min(pos0 + kUnit, p.old + p.n);  // its tokens that are new
+    const int j = pos0 >> g.log_p, place = pos0 & (g.P - 1);
+    int page;
+    if (j >= p.fresh) {
+      page = a.take[p.take + j - p.fresh];
+      if (place == 0 && lane == 0) claim_page(a.c, g, trow, j, page);
+    } else {
+      page = a.c.table[(size_t)trow * g.max_pages + j];
+    }
+    // source rows: lane t holds that of token pos0 + t
+    long long src = -1;
+    if (lane < kUnit && pos0 + lane >= t0 && pos0 + lane < t1) {
+      const int t = pos0 + lane - p.old;
+      const long long base = a.src_off ? a.src_off[row] : (long long)row * a.n_each;
+      src = base + (a.idx ? (long long)a.idx[a.idx_off[row] + t] : (long long)t);
+      if (src < 0 || src >= a.n_src) {
+        src = -1;
+        bad |= KV_DEV_RANGE;
+      }
+    }
+    if (page < 0 || page >= g.n_pages) {  // the same in every lane
+      bad |= KV_DEV_BOUNDS;
+      continue;
+    }
+    Row8<F32> k[ITER], v[ITER];
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+      const long long s = __shfl_sync(0xffffffffu, src, it * TPI + sub);
+      if (s >= 0) {
+        k[it].load(a.K, s, D, l);
+        v[it].load(a.V, s, D, l);
+      } else {
+        k[it].zero();
+        v[it].zero();
+      }
+    }
+    __syncwarp();  // the previous unit has left the stage
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+      const int t = it * TPI + sub;
+      float x[8];
+      uint32_t sc;
+      k[it].get(x);
+      uint32_t code = quantise8<QG / 8>(x, &sc);
+      reinterpret_cast<uint32_t*>(st)[t * (D / 8) + (l & 3) * W + (l >> 2)] = code;
+      if (l % (QG / 8) == 0) reinterpret_cast<uint32_t*>(st + 2 * kCode)[t * G + l / (QG / 8)] = sc;
+      v[it].get(x);
+      code = quantise8<QG / 8>(x, &sc);
+      const int pv = (2 * (l & 3)) ^ ((t & 2) << 1);  // place of channels 8 l .. 8 l + 3; the next four follow
+      uint16_t* sv = reinterpret_cast<uint16_t*>(st + kCode) + t * (D / 4) + pv * W + (l >> 2);
+      sv[0] = (uint16_t)code;
+      sv[W] = (uint16_t)(code >> 16);
+      if (l % (QG / 8) == 0) reinterpret_cast<uint32_t*>(st + 2 * kCode + kScale)[t * G + l / (QG / 8)] = sc;
+    }
+    __syncwarp();
+    uint8_t* pg = a.c.pages + (size_t)page * g.bytes;
+    const int f = t0 - pos0, e = t1 - pos0;  // tokens [f, e) of the unit
+    constexpr int RC = D / 2 / 16;           // 16-byte pieces of a token's codes
+    const uint4* sk = reinterpret_cast<const uint4*>(st);
+    uint4* dk = reinterpret_cast<uint4*>(pg + place * (D / 2));
+    uint4* dv = reinterpret_cast<uint4*>(pg + g.v + place * (D / 2));
+    for (int i = f * RC + lane; i < e * RC; i += 32) {
+      dk[i] = sk[i];
+      dv[i] = sk[i + kCode / 16];
+    }
+    const uint32_t* ss = reinterpret_cast<const uint32_t*>(st + 2 * kCode);
+    uint32_t* dks = reinterpret_cast<uint32_t*>(pg + g.ks) + place * G;
+    uint32_t* dvs = reinterpret_cast<uint32_t*>(pg + g.vs) + place * G;
+    for (int i = f * G + lane; i < e * G; i += 32) {
+      dks[i] = ss[i];
+      dvs[i] = ss[i + kScale / 4];
+    }
+  }
+  if (bad) atomicOr(a.c.status, bad);
+}
+
+// ---------------------------------------------------------------- reading
+struct LoadArgs {
+  PageGeom g;
+  SeqRows rows;
+  PagedCache c;
+  const int64_t* out_off;
+  long long n_out;
+  void* K;
+  void* V;
+};
+
+// Warps take runs of 16 output rows; lane t finds the token of output row t.
+template <int D, int QG, bool F32>
+__global__ void __launch_bounds__(kMoveWarps * 32) paged_load_kernel(const LoadArgs a) {
+  constexpr int G = D / QG, LT = D / 8, TPI = 32 / LT, ITER = kUnit / TPI, W = D / 32;
+  const PageGeom& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int l = lane % LT, sub = lane / LT;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int n_rows = a.rows.n_rows;
+  int bad = 0;
+  const long long first = a.out_off[0], last_ = a.out_off[n_rows];
+  const long long lo = max(first, 0ll), hi = min(last_, a.n_out);
+  if (first < 0 || last_ > a.n_out) bad |= KV_DEV_RANGE;
+  const long long units = hi > lo ? (hi - lo + kUnit - 1) / kUnit : 0;
+  const long long nw = (long long)gridDim.x * kMoveWarps, w = (long long)blockIdx.x * kMoveWarps + warp;
+  const long long u0 = w * units / nw, u1 = (w + 1) * units / nw;
+  int row = 0;
+  long long r0 = 0, r1 = -1;  // out_off of the row and of the next
+  for (long long u = u0; u < u1; ++u) {
+    const long long o0 = lo + u * kUnit, o = o0 + lane;
+    const uint8_t* pg = nullptr;
+    int place = 0;
+    if (lane < kUnit && o < hi) {
+      if (!(o >= r0 && o < r1)) {  // the last row that starts at or before o
+        int x = 0, y = n_rows - 1;
+        while (x < y) {
+          const int mid = (x + y + 1) >> 1;
+          if (a.out_off[mid] <= o) x = mid;
+          else y = mid - 1;
+        }
+        row = x;
+        r0 = a.out_off[row];
+        r1 = a.out_off[row + 1];
+      }
+      const int trow = table_row(a.rows, row);
+      const long long t = o - r0;
+      const int held = a.c.len[trow];
+      if (held < 0 || held > (g.max_pages << g.log_p)) bad |= KV_DEV_BOUNDS;
+      else if (t >= 0 && t < held && o < r1) {
+        const int page = a.c.table[(size_t)trow * g.max_pages + (t >> g.log_p)];
+        place = (int)(t & (g.P - 1));
+        if (page < 0 || page >= g.n_pages) bad |= KV_DEV_BOUNDS;
+        else pg = a.c.pages + (size_t)page * g.bytes;
+      }
+    }
+    uint32_t kc[ITER], vc[ITER], ksc[ITER], vsc[ITER];
+    bool have[ITER];
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+      const int t = it * TPI + sub;
+      const uint8_t* q = reinterpret_cast<const uint8_t*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(pg), t));
+      const int pl = __shfl_sync(0xffffffffu, place, t);
+      have[it] = q != nullptr;
+      kc[it] = vc[it] = ksc[it] = vsc[it] = 0;
+      if (have[it]) {
+        kc[it] = reinterpret_cast<const uint32_t*>(q + pl * (D / 2))[(l & 3) * W + (l >> 2)];
+        const int pv = (2 * (l & 3)) ^ ((pl & 2) << 1);
+        const uint16_t* hv = reinterpret_cast<const uint16_t*>(q + g.v + pl * (D / 2)) + pv * W + (l >> 2);
+        vc[it] = (uint32_t)hv[0] | ((uint32_t)hv[W] << 16);
+        ksc[it] = reinterpret_cast<const uint32_t*>(q + g.ks)[pl * G + l / (QG / 8)];
+        vsc[it] = reinterpret_cast<const uint32_t*>(q + g.vs)[pl * G + l / (QG / 8)];
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+      if (!have[it]) continue;
+      const long long orow = o0 + it * TPI + sub;
+      float x[8];
+      dequantise8(kc[it], ksc[it], x);
+      Row8<F32>::store(a.K, orow, D, l, x);
+      dequantise8(vc[it], vsc[it], x);
+      Row8<F32>::store(a.V, orow, D, l, x);
+    }
+  }
+  if (bad) atomicOr(a.c.status, bad);
+}
+
+// ---------------------------------------------------------- moving pages
+struct MoveArgs {
+  PageGeom g;     // of the destination
+  SeqRows dst, src;
+  PagedCache c;   // destination
+  const uint8_t* src_pages;
+  const int32_t* src_table;
+  int src_n_pages, src_max_pages;
+  const int32_t* idx;
+  const int64_t* idx_off;
+  const RowPlan* plan;
+  const int* unit;
+  const int* take;
+};
+
+constexpr int kRowThreads = 256;
+
+// Copies a page (a multiple of 16 bytes) with the whole block.
+__device__ __forceinline__ void copy_page(uint8_t* dst, const uint8_t* src, int bytes) {
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  const int n = bytes / 16;
+  for (int i = threadIdx.x; i < n; i += 4 * kRowThreads) {
+    uint4 v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (i + x * kRowThreads < n) v[x] = s[i + x * kRowThreads];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (i + x * kRowThreads < n) d[i + x * kRowThreads] = v[x];
+  }
+}
+
+// One CTA per destination row: the full pages gain a holder, the rest is copied.
+__global__ void __launch_bounds__(kRowThreads) paged_fork_kernel(const MoveArgs a) {
+  const PageGeom& g = a.g;
+  const int row = blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  const RowPlan p = a.plan[row];
+  if (p.fresh < 0) return;
+  const int td = table_row(a.dst, row), ts = table_row(a.src, row);
+  const int32_t* from = a.src_table + (size_t)ts * a.src_max_pages;
+  int32_t* to = a.c.table + (size_t)td * g.max_pages;
+  for (int j = threadIdx.x; j < p.fresh; j += kRowThreads) {
+    const int page = from[j];
+    to[j] = page;
+    if (page < 0 || page >= g.n_pages) atomicOr(a.c.status, KV_DEV_BOUNDS);
+    else atomicAdd(&a.c.ref[page], 1);
+  }
+  if (p.n & (g.P - 1)) {
+    const int page = from[p.fresh], fresh = a.take[p.take];
+    if (threadIdx.x == 0) claim_page(a.c, g, td, p.fresh, fresh);
+    if (page < 0 || page >= g.n_pages) {
+      if (threadIdx.x == 0) atomicOr(a.c.status, KV_DEV_BOUNDS);
+    } else {
+      copy_page(a.c.pages + (size_t)fresh * g.bytes, a.src_pages + (size_t)page * g.bytes, g.bytes);
+    }
+  }
+}
+
+// Every page of a row into a new one: grid (rows, slices); a slice's CTA takes every gridDim.y-th page.
+__global__ void __launch_bounds__(kRowThreads) paged_copy_kernel(const MoveArgs a) {
+  const PageGeom& g = a.g;
+  const int row = blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  const RowPlan p = a.plan[row];
+  if (p.fresh < 0) return;
+  const int td = table_row(a.dst, row), ts = table_row(a.src, row);
+  const int np = pages_of(g, p.n);
+  for (int j = blockIdx.y; j < np; j += gridDim.y) {
+    const int page = a.src_table[(size_t)ts * a.src_max_pages + j], fresh = a.take[p.take + j];
+    if (threadIdx.x == 0) claim_page(a.c, g, td, j, fresh);
+    if (page < 0 || page >= a.src_n_pages) {
+      if (threadIdx.x == 0) atomicOr(a.c.status, KV_DEV_BOUNDS);
+    } else {
+      copy_page(a.c.pages + (size_t)fresh * g.bytes, a.src_pages + (size_t)page * g.bytes, g.bytes);
+    }
+  }
+}
+
+// The kept tokens' codes and scales into the new pages, in units of 16 of the
+// tokens to be; a V row whose place differs in bit 1 has its halves swapped.
+// The lists change hands in paged_commit_kernel, when every token has moved.
+__global__ void __launch_bounds__(kMoveWarps * 32) paged_compact_kernel(const MoveArgs a) {
+  const PageGeom& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int n_rows = a.dst.n_rows;
+  const int total = a.unit[n_rows];
+  const long long nw = (long long)gridDim.x * kMoveWarps, w = (long long)blockIdx.x * kMoveWarps + warp;
+  const int u0 = (int)(w * total / nw), u1 = (int)((w + 1) * total / nw);
+  if (u0 >= u1) return;
+  const int rb = g.d / 2, rc = rb / 16;  // bytes and 16-byte pieces of a token's codes
+  int row = find_unit_row(a.unit, n_rows, u0);
+  int bad = 0;
+  for (int u = u0; u < u1; ++u) {
+    if (u >= a.unit[row + 1]) row = find_unit_row(a.unit, n_rows, u);
+    const RowPlan p = a.plan[row];
+    const int ts = table_row(a.src, row);
+    const int pos0 = (u - a.unit[row]) * kUnit, n = min(kUnit, p.n - pos0);
+    const int fresh = a.take[p.take + (pos0 >> g.log_p)], place0 = pos0 & (g.P - 1);
+    const uint8_t* from = nullptr;
+    int place = 0;
+    if (lane < n) {
+      const int pos = a.idx[a.idx_off[row] + pos0 + lane];
+      if (pos < 0 || pos >= p.old) {
+        bad |= KV_DEV_RANGE;
+      } else {
+        const int page = a.src_table[(size_t)ts * a.src_max_pages + (pos >> g.log_p)];
+        place = pos & (g.P - 1);
+        if (page < 0 || page >= g.n_pages) bad |= KV_DEV_BOUNDS;
+        else from = a.src_pages + (size_t)page * g.bytes;
+      }
+    }
+    uint8_t* to = a.c.pages + (size_t)fresh * g.bytes;
+    // 32 / rc tokens at a time (8 for d = 128, 16 for d = 64), a lane per piece
+    const int tpi = 32 / rc;
+    const int piece = lane & (rc - 1), sub = lane / rc;
+    for (int t0 = 0; t0 < n; t0 += tpi) {
+      const int t = t0 + sub;
+      const uint8_t* f = reinterpret_cast<const uint8_t*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), t & 31));
+      const int pl = __shfl_sync(0xffffffffu, place, t & 31);
+      if (t < n) {
+        uint4 k = make_uint4(0, 0, 0, 0), v = k;
+        const int to_place = place0 + t;
+        if (f) {
+          k = reinterpret_cast<const uint4*>(f + pl * rb)[piece];
+          const int vp = piece ^ (((pl ^ to_place) & 2) ? rc / 2 : 0);
+          v = reinterpret_cast<const uint4*>(f + g.v + pl * rb)[vp];
+        }
+        reinterpret_cast<uint4*>(to + to_place * rb)[piece] = k;
+        reinterpret_cast<uint4*>(to + g.v + to_place * rb)[piece] = v;
+      }
+    }
+    for (int i0 = 0; i0 < n * g.G; i0 += 32) {
+      const int i = i0 + lane, t = i / g.G, x = i - t * g.G;
+      const uint8_t* f = reinterpret_cast<const uint8_t*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), t & 31));
+      const int pl = __shfl_sync(0xffffffffu, place, t & 31);
+      if (i < n * g.G) {
+        const uint32_t ks = f ? reinterpret_cast<const uint32_t*>(f + g.ks)[pl * g.G + x] : 0u;
+        const uint32_t vs = f ? reinterpret_cast<const uint32_t*>(f + g.vs)[pl * g.G + x] : 0u;
+        reinterpret_cast<uint32_t*>(to + g.ks)[place0 * g.G + i] = ks;
+        reinterpret_cast<uint32_t*>(to + g.vs)[place0 * g.G + i] = vs;
+      }
+    }
+  }
+  if (bad) atomicOr(a.c.status, bad);
+}
+
+// After a compaction: a row replaced in place gives up its former pages, and the new ones enter the lists.
+__global__ void __launch_bounds__(kRowThreads) paged_commit_kernel(const MoveArgs a) {
+  const PageGeom& g = a.g;
+  const int row = blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  const RowPlan p = a.plan[row];
+  if (p.fresh < 0) return;
+  const int td = table_row(a.dst, row);
+  const int had = td == table_row(a.src, row) ? pages_of(g, p.old) : 0, has = pages_of(g, p.n);
+  for (int j = threadIdx.x; j < max(had, has); j += kRowThreads) {
+    if (j < had) drop_page(a.c, g, a.c.table[(size_t)td * g.max_pages + j]);
+    if (j < has) claim_page(a.c, g, td, j, a.take[p.take + j]);
+  }
+}
+
+// One CTA per row.
+__global__ void __launch_bounds__(kRowThreads)
+    paged_free_kernel(const PageGeom g, const SeqRows rows, const PagedCache c) {
+  const int trow = table_row(rows, blockIdx.x);
+  pdl_launch_dependents();
+  pdl_wait();
+  const int held = c.len[trow];
+  if (held < 0 || held > (g.max_pages << g.log_p)) {
+    if (threadIdx.x == 0) atomicOr(c.status, KV_DEV_BOUNDS);
+    return;
+  }
+  const int np = pages_of(g, held);
+  for (int j = threadIdx.x; j < np; j += kRowThreads) drop_page(c, g, c.table[(size_t)trow * g.max_pages + j]);
+  __syncthreads();  // every thread has read the length
+  if (threadIdx.x == 0) c.len[trow] = 0;
+}
+
+__global__ void __launch_bounds__(kRowThreads)
+    paged_count_kernel(const PageGeom g, int n_rows, const PagedCache c) {
+  for (int row = blockIdx.x; row < n_rows; row += gridDim.x) {
+    const int held = c.len[row];
+    if (held < 0 || held > (g.max_pages << g.log_p)) {
+      if (threadIdx.x == 0) atomicOr(c.status, KV_DEV_BOUNDS);
+      continue;
+    }
+    const int np = pages_of(g, held);
+    for (int j = threadIdx.x; j < np; j += kRowThreads) {
+      const int page = c.table[(size_t)row * g.max_pages + j];
+      if (page < 0 || page >= g.n_pages) atomicOr(c.status, KV_DEV_BOUNDS);
+      else atomicAdd(&c.ref[page], 1);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kRowThreads) paged_bits_kernel(int n_pages, const PagedCache c) {
+  const int words = (n_pages + 31) >> 5;
+  const int lane = threadIdx.x & 31;
+  const int nw = (gridDim.x * kRowThreads) >> 5;
+  for (int w = (blockIdx.x * kRowThreads + threadIdx.x) >> 5; w < words; w += nw) {
+    const int page = (w << 5) + lane;
+    const unsigned b = __ballot_sync(0xffffffffu, page < n_pages && c.ref[page] == 0);
+    if (lane == 0) c.free_bits[w] = b;
+  }
+}
+
+// ------------------------------------------------------------------- host
+bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+bool cache_ok(const kv_paged_cache* c) {
+  return c && aligned16(c->pages) && aligned16(c->table) && aligned16(c->len) && aligned16(c->ref) &&
+         aligned16(c->free_bits) && c->status && (reinterpret_cast<uintptr_t>(c->status) & 3) == 0;
+}
+
+PagedCache cache_of(const kv_paged_cache& c) {
+  return {static_cast<uint8_t*>(c.pages), c.table, c.len, c.ref, c.free_bits, c.status};
+}
+
+// The rows of a call; false when a sequence or layer is outside the cache, or (distinct) named twice.
+bool make_rows(const kv_paged_shape& sh, const int32_t* seq, int32_t n, int layer0, int n_lay, bool distinct,
+               SeqRows* r) {
+  if (!seq || n < 1 || n > KV_MAX_SEQ) return false;
+  if (layer0 < 0 || n_lay < 1 || layer0 > sh.n_layers - n_lay) return false;
+  for (int i = 0; i < n; ++i) {
+    if (seq[i] < 0 || seq[i] >= sh.n_seqs) return false;
+    if (distinct)
+      for (int j = 0; j < i; ++j)
+        if (seq[j] == seq[i]) return false;
+  }
+  r->n_seq = n;
+  r->per_seq = n_lay * sh.n_kv_heads;
+  r->first = layer0 * sh.n_kv_heads;
+  r->table_rps = sh.n_layers * sh.n_kv_heads;
+  r->n_rows = n * r->per_seq;
+  for (int i = 0; i < KV_MAX_SEQ; ++i) r->seq[i] = i < n ? seq[i] : 0;
+  return true;
+}
+
+// Launch whose set-up overlaps the previous kernel's tail. Every kernel here waits for that kernel before it touches
+// memory, and reads with plain loads (the read-only path may not see what a kernel that was still running wrote).
+template <class... P, class... A>
+int launch(void (*k)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, k, P(args)...));
+}
+
+template <int D, int QG>
+int store_as(bool f32, int grid, const StoreArgs& a, cudaStream_t st) {
+  return f32 ? launch(paged_store_kernel<D, QG, true>, grid, kMoveWarps * 32, st, a)
+             : launch(paged_store_kernel<D, QG, false>, grid, kMoveWarps * 32, st, a);
+}
+template <int D, int QG>
+int load_as(bool f32, int grid, const LoadArgs& a, cudaStream_t st) {
+  return f32 ? launch(paged_load_kernel<D, QG, true>, grid, kMoveWarps * 32, st, a)
+             : launch(paged_load_kernel<D, QG, false>, grid, kMoveWarps * 32, st, a);
+}
+
+struct Ws {
+  RowPlan* plan;
+  int* unit;
+  int* take;
+};
+Ws ws_of(const kv_paged_shape& sh, void* ws) {
+  const PagedWs w = paged_ws_layout(sh);
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  return {reinterpret_cast<RowPlan*>(p + w.plan), reinterpret_cast<int*>(p + w.unit),
+          reinterpret_cast<int*>(p + w.take)};
+}
+
+bool ws_ok(const kv_paged_shape& sh, const kv_paged_cache& c) {
+  return aligned16(c.ws) && c.ws_bytes >= paged_ws_layout(sh).bytes;
+}
+
+// The rows of src -> dst lists: dst distinct, and no dst a src of its own cache except (in_place) its own entry's.
+bool lists_ok(const int32_t* src, const int32_t* dst, int32_t n, bool same_cache, bool in_place) {
+  if (!same_cache) return true;
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n; ++j)
+      if (dst[i] == src[j] && !(in_place && i == j)) return false;
+  return true;
+}
+
+}  // namespace
+}  // namespace kvc
+
+using namespace kvc;
+
+extern "C" {
+
+size_t kv_paged_page_bytes(const kv_paged_shape* shape) {
+  return paged_shape_ok(shape) ? (size_t)page_geom(*shape).bytes : 0;
+}
+
+size_t kv_paged_ws_bytes(const kv_paged_shape* shape) {
+  return paged_shape_ok(shape) ? paged_ws_layout(*shape).bytes : 0;
+}
+
+int kv_paged_rebuild(const kv_paged_shape* shape, const kv_paged_cache* cache, void* stream) {
+  if (fault_injected("kv_paged_rebuild")) return KV_ERR_CUDA;
+  if (!paged_shape_ok(shape) || !cache_ok(cache)) return KV_ERR_ARG;
+  if (!ws_ok(*shape, *cache)) return KV_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const PageGeom g = page_geom(*shape);
+  const PagedCache c = cache_of(*cache);
+  const int rows = shape->n_seqs * shape->n_layers * shape->n_kv_heads;
+  if (cudaMemsetAsync(c.ref, 0, (size_t)g.n_pages * sizeof(int32_t), st) != cudaSuccess) return KV_ERR_CUDA;
+  const int cap = sm_count() * 8;
+  paged_count_kernel<<<rows < cap ? rows : cap, kRowThreads, 0, st>>>(g, rows, c);
+  const int blocks = (g.n_pages + kRowThreads - 1) / kRowThreads;
+  paged_bits_kernel<<<blocks < cap ? blocks : cap, kRowThreads, 0, st>>>(g.n_pages, c);
+  return cuda_status(cudaGetLastError());
+}
+
+int kv_paged_append(const kv_paged_shape* shape, const kv_paged_cache* cache, const int32_t* seq, int32_t n_seq,
+                    int32_t layer0, int32_t n_lay, const void* K, const void* V, int64_t n_src, int32_t n_each,
+                    const int32_t* count, const int64_t* src_off, const int32_t* idx, const int64_t* idx_off,
+                    void* stream) {
+  if (fault_injected("kv_paged_append")) return KV_ERR_CUDA;
+  if (!paged_shape_ok(shape) || !cache_ok(cache)) return KV_ERR_ARG;
+  PlanArgs p = {};
+  if (!make_rows(*shape, seq, n_seq, layer0, n_lay, true, &p.dst)) return KV_ERR_ARG;
+  if (!aligned16(K) || !aligned16(V) || n_src < 0 || n_each < 0) return KV_ERR_ARG;
+  if (count && !src_off) return KV_ERR_ARG;
+  if (idx && (!src_off || !idx_off)) return KV_ERR_ARG;
+  if (!ws_ok(*shape, *cache)) return KV_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Ws w = ws_of(*shape, cache->ws);
+  p.g = page_geom(*shape);
+  p.c = cache_of(*cache);
+  p.count = count;
+  p.n_each = n_each;
+  p.plan = w.plan, p.unit = w.unit, p.take = w.take;
+  int rc = launch(paged_plan_kernel<kAppend>, 1, kPlanThreads, st, p);
+  if (rc) return rc;
+  StoreArgs a = {p.g, p.dst, p.c, K, V, n_src, n_each, src_off, idx, idx_off, w.plan, w.unit, w.take};
+  // a unit per warp while that leaves SMs idle; the batch's units are known on the device only, n_src bounds them
+  const long long warps = n_src / kUnit + 2ll * p.dst.n_rows;
+  const long long want = (warps + kMoveWarps - 1) / kMoveWarps, cap = 4ll * sm_count();
+  const int grid = (int)(want < cap ? want : cap);
+  const bool f32 = shape->dtype == KV_F32;
+  if (shape->head_dim == 64) return shape->quant_group == 32 ? store_as<64, 32>(f32, grid, a, st) : store_as<64, 64>(f32, grid, a, st);
+  return shape->quant_group == 32   ? store_as<128, 32>(f32, grid, a, st)
+         : shape->quant_group == 64 ? store_as<128, 64>(f32, grid, a, st)
+                                    : store_as<128, 128>(f32, grid, a, st);
+}
+
+int kv_paged_load(const kv_paged_shape* shape, const kv_paged_cache* cache, const int32_t* seq, int32_t n_seq,
+                  int32_t layer0, int32_t n_lay, const int64_t* out_off, int64_t n_out, void* K_out, void* V_out,
+                  void* stream) {
+  if (fault_injected("kv_paged_load")) return KV_ERR_CUDA;
+  if (!paged_shape_ok(shape) || !cache_ok(cache)) return KV_ERR_ARG;
+  LoadArgs a = {};
+  if (!make_rows(*shape, seq, n_seq, layer0, n_lay, true, &a.rows)) return KV_ERR_ARG;
+  if (!out_off || (reinterpret_cast<uintptr_t>(out_off) & 7) || n_out < 0 || !aligned16(K_out) || !aligned16(V_out))
+    return KV_ERR_ARG;
+  if (!ws_ok(*shape, *cache)) return KV_ERR_WORKSPACE;
+  a.g = page_geom(*shape);
+  a.c = cache_of(*cache);
+  a.out_off = out_off, a.n_out = n_out, a.K = K_out, a.V = V_out;
+  const long long want = (n_out / kUnit + kMoveWarps) / kMoveWarps, cap = 8ll * sm_count();
+  const int grid = (int)(want < cap ? want : cap);
+  const bool f32 = shape->dtype == KV_F32;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (shape->head_dim == 64) return shape->quant_group == 32 ? load_as<64, 32>(f32, grid, a, st) : load_as<64, 64>(f32, grid, a, st);
+  return shape->quant_group == 32   ? load_as<128, 32>(f32, grid, a, st)
+         : shape->quant_group == 64 ? load_as<128, 64>(f32, grid, a, st)
+                                    : load_as<128, 128>(f32, grid, a, st);
+}
+
+int kv_paged_attn(const kv_paged_shape* shape, const kv_paged_cache* cache, const int32_t* seq, int32_t n_seq,
+                  int32_t layer0, int32_t n_lay, int32_t n_q, const void* q, void* out, float* lse, void* stream) {
+  if (fault_injected("kv_paged_attn")) return KV_ERR_CUDA;
+  if (!paged_shape_ok(shape) || !cache_ok(cache)) return KV_ERR_ARG;
+  SeqRows rows;
+  if (!make_rows(*shape, seq, n_seq, layer0, n_lay, true, &rows)) return KV_ERR_ARG;
+  if (n_q < 1 || n_q > KV_PAGED_MAX_QUERIES || n_q * shape->group > KV_PAGED_MAX_QUERIES) return KV_ERR_ARG;
+  if (!aligned16(q) || !aligned16(out) || q == out) return KV_ERR_ARG;
+  if (lse && (reinterpret_cast<uintptr_t>(lse) & 3)) return KV_ERR_ARG;
+  if (!ws_ok(*shape, *cache)) return KV_ERR_WORKSPACE;
+  return launch_paged_attn(*shape, page_geom(*shape), rows, cache_of(*cache), static_cast<uint8_t*>(cache->ws), n_q, q,
+                           out, lse, static_cast<cudaStream_t>(stream));
+}
+
+int kv_paged_fork(const kv_paged_shape* shape, const kv_paged_cache* cache, const int32_t* src, const int32_t* dst,
+                  int32_t n, void* stream) {
+  if (fault_injected("kv_paged_fork")) return KV_ERR_CUDA;
+  if (!paged_shape_ok(shape) || !cache_ok(cache)) return KV_ERR_ARG;
+  PlanArgs p = {};
+  if (!make_rows(*shape, src, n, 0, shape->n_layers, false, &p.src) ||
+      !make_rows(*shape, dst, n, 0, shape->n_layers, true, &p.dst) || !lists_ok(src, dst, n, true, false))
+    return KV_ERR_ARG;
+  if (!ws_ok(*shape, *cache)) return KV_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Ws w = ws_of(*shape, cache->ws);
+  p.g = page_geom(*shape);
+  p.c = cache_of(*cache);
+  p.src_len = cache->len;
+  p.src_max = shape->max_pages * shape->page_tokens;
+  p.plan = w.plan, p.unit = w.unit, p.take = w.take;
+  int rc = launch(paged_plan_kernel<kFork>, 1, kPlanThreads, st, p);
+  if (rc) return rc;
+  MoveArgs a = {p.g,           p.dst,            p.src,   p.c,     p.c.pages, p.c.table,
+                shape->n_pages, shape->max_pages, nullptr, nullptr, w.plan,    w.unit,    w.take};
+  return launch(paged_fork_kernel, p.dst.n_rows, kRowThreads, st, a);
+}
+
+// The address a kernel reaches pages at: device or managed memory as is, pinned host memory at its device mapping.
+static uint8_t* pages_address(void* p) {
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  if (at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged) return static_cast<uint8_t*>(p);
+  if (at.type == cudaMemoryTypeHost && at.devicePointer) return static_cast<uint8_t*>(at.devicePointer);
+  return nullptr;
+}
+
+int kv_paged_copy(const kv_paged_shape* src_shape, const kv_paged_cache* src_cache, const int32_t* src,
+                  const kv_paged_shape* dst_shape, const kv_paged_cache* dst_cache, const int32_t* dst, int32_t n,
+                  void* stream) {
+  if (fault_injected("kv_paged_copy")) return KV_ERR_CUDA;
+  if (!paged_shape_ok(src_shape) || !paged_shape_ok(dst_shape) || !cache_ok(src_cache) || !cache_ok(dst_cache))
+    return KV_ERR_ARG;
+  if (src_shape->n_layers != dst_shape->n_layers || src_shape->n_kv_heads != dst_shape->n_kv_heads ||
+      src_shape->head_dim != dst_shape->head_dim || src_shape->quant_group != dst_shape->quant_group ||
+      src_shape->page_tokens != dst_shape->page_tokens)
+    return KV_ERR_ARG;
+  PlanArgs p = {};
+  if (!make_rows(*src_shape, src, n, 0, src_shape->n_layers, false, &p.src) ||
+      !make_rows(*dst_shape, dst, n, 0, dst_shape->n_layers, true, &p.dst) ||
+      !lists_ok(src, dst, n, src_cache->table == dst_cache->table, false))
+    return KV_ERR_ARG;
+  if (!ws_ok(*dst_shape, *dst_cache)) return KV_ERR_WORKSPACE;
+  uint8_t* sp = pages_address(src_cache->pages);
+  uint8_t* dp = pages_address(dst_cache->pages);
+  if (!sp || !dp) return KV_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Ws w = ws_of(*dst_shape, dst_cache->ws);
+  p.g = page_geom(*dst_shape);
+  p.c = cache_of(*dst_cache);
+  p.c.pages = dp;
+  p.src_len = src_cache->len;
+  p.src_max = src_shape->max_pages * src_shape->page_tokens;
+  p.plan = w.plan, p.unit = w.unit, p.take = w.take;
+  int rc = launch(paged_plan_kernel<kCopy>, 1, kPlanThreads, st, p);
+  if (rc) return rc;
+  MoveArgs a = {p.g,   p.dst, p.src,  p.c,    sp, src_cache->table, src_shape->n_pages, src_shape->max_pages, nullptr,
+                nullptr, w.plan, w.unit, w.take};
+  // enough CTAs to fill the SMs when rows are few
+  const int want = 8 * sm_count() / p.dst.n_rows + 1;
+  const int slices = want < dst_shape->max_pages ? want : dst_shape->max_pages;
+  return launch(paged_copy_kernel, dim3(p.dst.n_rows, slices), kRowThreads, st, a);
+}
+
+int kv_paged_compact(const kv_paged_shape* shape, const kv_paged_cache* cache, const int32_t* src,
+                     const int32_t* dst, int32_t n, const int32_t* idx, const int64_t* idx_off,
+                     const int32_t* count, void* stream) {
+  if (fault_injected("kv_paged_compact")) return KV_ERR_CUDA;
+  if (!paged_shape_ok(shape) || !cache_ok(cache)) return KV_ERR_ARG;
+  PlanArgs p = {};
+  if (!make_rows(*shape, src, n, 0, shape->n_layers, false, &p.src) ||
+      !make_rows(*shape, dst, n, 0, shape->n_layers, true, &p.dst) || !lists_ok(src, dst, n, true, true))
+    return KV_ERR_ARG;
+  if (!idx || !idx_off || !count) return KV_ERR_ARG;
+  if (!ws_ok(*shape, *cache)) return KV_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Ws w = ws_of(*shape, cache->ws);
+  p.g = page_geom(*shape);
+  p.c = cache_of(*cache);
+  p.src_len = cache->len;
+  p.src_max = shape->max_pages * shape->page_tokens;
+  p.count = count;
+  p.plan = w.plan, p.unit = w.unit, p.take = w.take;
+  int rc = launch(paged_plan_kernel<kCompact>, 1, kPlanThreads, st, p);
+  if (rc) return rc;
+  MoveArgs a = {p.g,           p.dst,            p.src, p.c,     p.c.pages, p.c.table,
+                shape->n_pages, shape->max_pages, idx,   idx_off, w.plan,    w.unit,    w.take};
+  const long long want = ((long long)shape->n_pages * shape->page_tokens / kUnit + kMoveWarps - 1) / kMoveWarps;
+  const long long cap = 8ll * sm_count();
+  rc = launch(paged_compact_kernel, (int)(want < cap ? want : cap), kMoveWarps * 32, st, a);
+  if (rc) return rc;
+  return launch(paged_commit_kernel, p.dst.n_rows, kRowThreads, st, a);
+}
+
+int kv_paged_free(const kv_paged_shape* shape, const kv_paged_cache* cache, const int32_t* seq, int32_t n_seq,
+                  void* stream) {
+  if (fault_injected("kv_paged_free")) return KV_ERR_CUDA;
+  if (!paged_shape_ok(shape) || !cache_ok(cache)) return KV_ERR_ARG;
+  SeqRows rows;
+  if (!make_rows(*shape, seq, n_seq, 0, shape->n_layers, true, &rows)) return KV_ERR_ARG;
+  return launch(paged_free_kernel, rows.n_rows, kRowThreads, static_cast<cudaStream_t>(stream), page_geom(*shape),
+                rows, cache_of(*cache));
+}
+
+}  // extern "C"

@@ -1,0 +1,715 @@
+// kv_paged_attn: attention of a few query tokens per row over the paged 4-bit
+// cache (formats in include/kvcomp_paged.h).
+//
+// What bounds it: the codes and scales are read once, d + 8 G bytes a token
+// (144 at d = 128 and groups of 64); the arithmetic to unpack them is near the
+// SMs' issue rate at that bandwidth, so the inner loop is kept to about an
+// instruction a code.
+//
+// Products. Codes go to the tensor cores as bf16 without a conversion: bits
+// 0-3 of a 16-bit half or-ed into 0x4300 are the bf16 number 128 + c exactly.
+// With a group's step s and base m taken out of the sums,
+//   q.k = sum_g s_g (q.(128 + c))_g + (m_g - 128 s_g) (sum of q over g),
+//   sum_j p_j v_j = sum_j p'_j (128 + c_j) - 128 sum_j p'_j + sum_j p_j m_j,
+// p'_j = p_j s_j rounded to bf16 (its sum is that of the rounded numbers, so
+// the rounding is the only error: at most 2^-8 of a term). fp32 caches take c itself
+// (one subtraction a pair) and split q and p' into three bf16 parts each, which
+// together hold their 24 bits. Both products have the cache as the 16-row
+// operand (mma.sync m16n8k16: keys x queries, then channels x queries), so up
+// to 8 queries cost no padding; a warp's fragments are one 16-byte load of K
+// codes a key and 8-byte loads of V codes, free of bank conflicts by the
+// page's order of words and the order in which a tile's keys take the rows.
+//
+// Work. Rows are cut into tiles of 64 tokens; a row costs its tiles plus one.
+// The CTAs (up to three per SM) take equal shares of the total, contiguous
+// over rows; in a CTA one warp streams tiles into a ring of stages with bulk
+// copies (the four parts of a page's 64 tokens are each contiguous) and four
+// warps take 16 tokens of a tile each, with a softmax of their own that is
+// joined when the CTA leaves the row. A row that several CTAs share leaves
+// partials, joined by paged_combine_kernel in CTA order. Every sum has a fixed
+// order.
+#include "paged_common.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int kTile = 64;     // tokens per tile
+constexpr int kWarps = 4;     // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kStages = 5;
+constexpr float kGrow = 8.f;  // the running maximum moves when a logit passes it by this (log2 units)
+
+struct AttnArgs {
+  PageGeom g;
+  SeqRows rows;
+  PagedCache c;
+  int row0, n_rows;  // call rows of this launch
+  int n_q, group, R; // R = n_q * group
+  float scale2;      // log2(e) / sqrt(d)
+  const void* q;
+  void* out;
+  float* lse;
+  int4* split;       // [CTAs]: a row whose second CTA this is (row, first CTA, last CTA), or -1
+  float* part;
+  unsigned long long limit_ns;
+};
+
+// Shared memory of a CTA.
+template <int D, int NG, int NT>
+struct Smem {
+  static constexpr int kCode = kTile * D / 2, kScale = kTile * NG * 4;
+  static constexpr int kV = kCode, kKs = 2 * kCode, kVs = kKs + kScale, kStage = kVs + kScale;
+  static constexpr int NQ = NT * 8, kORow = D + 4;
+  static constexpr int kObuf = kStages * kStage;
+  static constexpr int kMl = kObuf + kWarps * NQ * kORow * 4;
+  static constexpr int kBase = kMl + kWarps * NQ * 8;
+  static constexpr int kBar = (kBase + (kAttnRows + 1) * 4 + 15) / 16 * 16;
+  static constexpr int kBytes = kBar + 2 * kStages * 8 + 64;
+};
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// Nibble pair n of x (bits 4 n and 16 + 4 n) as two bf16: 128 + c, or c itself.
+template <bool PLAIN>
+__device__ __forceinline__ uint32_t codes2(uint32_t x, int n) {
+  const uint32_t r = ((x >> (4 * n)) & 0x000f000fu) | 0x43004300u;
+  if (!PLAIN) return r;
+  const uint32_t b = 0x43004300u;
+  const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&r), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// CTAs that share the work: at least two tiles' cost each.
+__device__ __forceinline__ int cta_count(int cost, int grid) { return max(1, min(grid, (cost + 1) / 2)); }
+
+template <int D, int NG, int NT, bool F32>
+__global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2) paged_attn_kernel(const AttnArgs a) {
+  using S = Smem<D, NG, NT>;
+  constexpr int W = D / 32, NQ = S::NQ, PARTS = F32 ? 3 : 1;
+  constexpr float BIAS = F32 ? 0.f : 128.f;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* obuf = reinterpret_cast<float*>(smem + S::kObuf);
+  float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
+  int* base = reinterpret_cast<int*>(smem + S::kBase);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBar);
+  uint64_t* empty = full + kStages;
+  int* wsum = reinterpret_cast<int*>(empty + kStages);
+  volatile int* abort_flag = wsum + 8;
+  const PageGeom& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWarps);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // base[i]: cost of the rows before row i; every thread sums a run of rows
+  {
+    const int per = (a.n_rows + kThreads - 1) / kThreads;
+    const int i0 = threadIdx.x * per, i1 = min(a.n_rows, i0 + per);
+    int sum = 0;
+    for (int i = i0; i < i1; ++i) {
+      int n = a.c.len[table_row(a.rows, a.row0 + i)];
+      if (n < 0 || n > (g.max_pages << g.log_p)) {
+        n = 0;
+        if (blockIdx.x == 0) atomicOr(a.c.status, KV_DEV_BOUNDS);
+      }
+      base[i] = sum;  // made absolute below
+      sum += (n + kTile - 1) / kTile + 1;
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int before = incl - sum;
+    for (int i = 0; i < warp; ++i) before += wsum[i];
+    for (int i = i0; i < i1; ++i) base[i] += before;
+    if (i1 == a.n_rows && i0 < a.n_rows) base[a.n_rows] = before + sum;
+    __syncthreads();
+  }
+  const int cost = base[a.n_rows];
+  const int n_cta = cta_count(cost, gridDim.x);
+  const int cta = blockIdx.x;
+  const int chunk = blockIdx.y;  // of NQ query rows
+  if (cta >= n_cta) {
+    if (threadIdx.x == 0 && chunk == 0) a.split[cta] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  const int lo = (int)((long long)cost * cta / n_cta), hi = (int)((long long)cost * (cta + 1) / n_cta);
+  int row = 0;
+  {
+    int x = 0, y = a.n_rows - 1;  // the last row with base <= lo
+    while (x < y) {
+      const int mid = (x + y + 1) >> 1;
+      if (base[mid] <= lo) x = mid;
+      else y = mid - 1;
+    }
+    row = x;
+  }
+  if (threadIdx.x == 0 && chunk == 0) {
+    const int t0 = lo - base[row] - 1;  // > 0: the row's first tiles are another CTA's
+    int4 rec = make_int4(-1, 0, 0, 0);
+    if (t0 > 0) {
+      const int f = (int)(((long long)(base[row] + 2) * n_cta - 1) / cost);  // holds the row's first tile
+      const int l = (int)(((long long)base[row + 1] * n_cta - 1) / cost);    // holds its last
+      if (f + 1 == cta) rec = make_int4(row, f, l, 0);
+    }
+    a.split[cta] = rec;
+  }
+  const Guard guard{abort_flag, a.c.status, a.limit_ns};
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    const int part_tokens = min(g.P, kTile), ppt = kTile / part_tokens;  // pages per tile
+    const int pg = lane >> 2, sec = lane & 3;
+    const bool mine = pg < ppt;
+    const uint32_t sec_bytes = sec < 2 ? part_tokens * (D / 2) : part_tokens * NG * 4;
+    const int sec_page = sec == 0 ? 0 : sec == 1 ? g.v : sec == 2 ? g.ks : g.vs;
+    const int sec_stage = sec == 0 ? 0 : sec == 1 ? S::kV : sec == 2 ? S::kKs : S::kVs;
+    const uint32_t tok_bytes = sec < 2 ? D / 2 : NG * 4;
+    int it = 0;
+    bool ok = true;
+    for (int r = row; ok && r < a.n_rows && base[r] < hi; ++r) {
+      const int tiles = base[r + 1] - base[r] - 1;
+      const int t0 = max(lo - base[r] - 1, 0), t1 = min(tiles, hi - base[r] - 1);
+      if (t0 >= t1) continue;
+      const int trow = table_row(a.rows, a.row0 + r);
+      const int32_t* list = a.c.table + (size_t)trow * g.max_pages;
+      const int np = (a.c.len[trow] + g.P - 1) >> g.log_p;
+      int win = -32, entry = 0;  // lane l holds page number list[win + l]
+      for (int t = t0; t < t1; ++t, ++it) {
+        const int j0 = (t * kTile) >> g.log_p;
+        if (j0 + ppt > win + 32) {
+          win = j0;
+          entry = win + lane < np ? list[win + lane] : -1;
+        }
+        const int page = __shfl_sync(0xffffffffu, entry, min(31, j0 - win + pg));
+        const bool there = mine && j0 + pg < np;
+        const bool good = there && page >= 0 && page < g.n_pages;
+        if (there && !good) atomicOr(a.c.status, KV_DEV_BOUNDS);
+        const int s = it % kStages;
+        if (it >= kStages) ok = wait_bounded(&empty[s], ((it / kStages) - 1) & 1, guard);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const unsigned n_good = __popc(__ballot_sync(0xffffffffu, good && sec == 0));
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], n_good * part_tokens * (D + 8 * NG));
+        __syncwarp();
+        if (good) {
+          const uint8_t* src =
+              a.c.pages + (size_t)page * g.bytes + sec_page + ((t * kTile) & (g.P - 1)) * tok_bytes;
+          bulk_load(smem + s * S::kStage + sec_stage + pg * part_tokens * tok_bytes, src, sec_bytes, &full[s]);
+        }
+      }
+    }
+    // copies in flight land before the CTA gives its memory back, also when the others have given up
+    for (int k = max(0, it - kStages); k < it; ++k) wait_drain(&full[k % kStages], (k / kStages) & 1);
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int grp = lane >> 2, tig = lane & 3;
+  // Matrix row r of a half tile is token tok(r): rows 2 t and 2 t + 1 are tokens t and 4 + (t ^ 1), so that the
+  // lanes of a K load and of a V load fall on different banks.
+  const int krow = warp * 16 + ((grp & 1) ? 4 + ((grp >> 1) ^ 1) : grp >> 1);
+  const int vrow = warp * 16 + tig, vrow2 = warp * 16 + 4 + (tig ^ 1);
+  const int vplace = grp ^ ((tig & 2) << 1);
+  int it = 0;
+  bool ok = true;
+  for (int r = row; r < a.n_rows && base[r] < hi; ++r) {
+    const int tiles = base[r + 1] - base[r] - 1;
+    const int t0 = max(lo - base[r] - 1, 0), t1 = min(tiles, hi - base[r] - 1);
+    const int crow = a.row0 + r;
+    if (tiles > 0 && t0 >= t1) continue;
+    const int q0 = chunk * NQ, nq = min(NQ, a.R - q0);
+    const int len = tiles > 0 ? a.c.len[table_row(a.rows, crow)] : 0;
+
+    // query fragments and their sums by group
+    uint32_t qf[NT][PARTS][W][4];
+    float qsum[NT][NG][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int qi = nt * 8 + grp;
+      float sum[NG];
+#pragma unroll
+      for (int x = 0; x < NG; ++x) sum[x] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        float x[8];
+        const long long at = ((long long)crow * a.R + q0 + qi) * D + 32 * w + 8 * tig;
+        if (qi < nq) {
+          if (F32) {
+            const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 4);
+            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+          } else {
+            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+            x[0] = lo_f(u.x), x[1] = hi_f(u.x), x[2] = lo_f(u.y), x[3] = hi_f(u.y);
+            x[4] = lo_f(u.z), x[5] = hi_f(u.z), x[6] = lo_f(u.w), x[7] = hi_f(u.w);
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < 8; ++n) x[n] = 0.f;
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) sum[w * NG / W] += x[n];
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {  // a code pair holds channels n and n + 4
+            qf[nt][p][w][n] = pack2(x[n], x[n + 4]);
+            if (F32) {
+              x[n] -= lo_f(qf[nt][p][w][n]);
+              x[n + 4] -= hi_f(qf[nt][p][w][n]);
+            }
+          }
+      }
+#pragma unroll
+      for (int x = 0; x < NG; ++x) {
+        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
+        qsum[nt][x][0] = __shfl_sync(0xffffffffu, sum[x], (2 * tig) * 4);
+        qsum[nt][x][1] = __shfl_sync(0xffffffffu, sum[x], (2 * tig + 1) * 4);
+      }
+    }
+    // keys that this lane's queries see
+    int lim[NT][2];
+    const int lim_min = len - a.n_q + 1;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int qi = nt * 8 + 2 * tig + x;
+        lim[nt][x] = qi < nq ? lim_min + (q0 + qi) / a.group : len;
+      }
+
+    float O[NT][2 * W][4], psum[NT][NG][4], off[NT][NG][2], m2[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int x = 0; x < 2 * W; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) O[nt][x][y] = 0.f;
+#pragma unroll
+      for (int x = 0; x < NG; ++x) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) psum[nt][x][y] = 0.f;
+        off[nt][x][0] = off[nt][x][1] = 0.f;
+      }
+      m2[nt][0] = m2[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    for (int t = t0; ok && t < t1; ++t, ++it) {
+      const int s = it % kStages;
+      ok = wait_bounded(&full[s], (it / kStages) & 1, guard);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint8_t* st = smem + s * S::kStage;
+      const int tok0 = t * kTile + warp * 16;
+      const bool some = tok0 < len;                // the warp's tokens hold keys
+      const bool masked = tok0 + 16 > lim_min;     // some of them are hidden from some query
+      const int key0 = tok0 + krow - warp * 16;    // keys of matrix rows grp and grp + 8: key0, key0 + 8
+      if (some) {
+        // ---- logits: rows keys, columns queries
+        uint32_t kw[2][W], ks[2][NG];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint8_t* kp = st + (krow + 8 * x) * (D / 2) + tig * (D / 8);
+          if (W == 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(kp);
+            kw[x][0] = u.x, kw[x][1] = u.y, kw[x][W - 2] = u.z, kw[x][W - 1] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(kp);
+            kw[x][0] = u.x, kw[x][1] = u.y;
+          }
+          const uint8_t* sp = st + S::kKs + (krow + 8 * x) * (NG * 4);
+          if (NG == 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(sp);
+            ks[x][0] = u.x, ks[x][NG > 1 ? 1 : 0] = u.y, ks[x][NG > 2 ? 2 : 0] = u.z, ks[x][NG > 3 ? 3 : 0] = u.w;
+          } else if (NG == 2) {
+            const uint2 u = *reinterpret_cast<const uint2*>(sp);
+            ks[x][0] = u.x, ks[x][NG > 1 ? 1 : 0] = u.y;
+          } else {
+            ks[x][0] = *reinterpret_cast<const uint32_t*>(sp);
+          }
+        }
+        float acc[NT][NG][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < NG; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) acc[nt][x][y] = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          uint32_t c0[4], c1[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            c0[n] = codes2<F32>(kw[0][w], n);
+            c1[n] = codes2<F32>(kw[1][w], n);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int p = PARTS - 1; p >= 0; --p) {
+              mma(acc[nt][w * NG / W], c0[0], c1[0], c0[1], c1[1], qf[nt][p][w][0], qf[nt][p][w][1]);
+              mma(acc[nt][w * NG / W], c0[2], c1[2], c0[3], c1[3], qf[nt][p][w][2], qf[nt][p][w][3]);
+            }
+        }
+        float y[NT][4];
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) y[nt][x] = 0.f;
+#pragma unroll
+          for (int x = 0; x < NG; ++x)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const float sc = lo_f(ks[z][x]), ad = fmaf(-BIAS, sc, hi_f(ks[z][x]));
+              y[nt][2 * z] = fmaf(sc, acc[nt][x][2 * z], fmaf(ad, qsum[nt][x][0], y[nt][2 * z]));
+              y[nt][2 * z + 1] = fmaf(sc, acc[nt][x][2 * z + 1], fmaf(ad, qsum[nt][x][1], y[nt][2 * z + 1]));
+            }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            y[nt][x] *= a.scale2;
+            if (masked && key0 + 8 * (x >> 1) >= lim[nt][x & 1]) y[nt][x] = -INFINITY;
+            grow |= y[nt][x] > m2[nt][x & 1] + kGrow;
+          }
+        }
+        // ---- softmax: the running maximum follows only when a logit passes it by far
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float mx = fmaxf(y[nt][x], y[nt][2 + x]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              const float now = fmaxf(m2[nt][x], mx);
+              const float f = now == m2[nt][x] ? 1.f : ex2_approx(m2[nt][x] - now);
+              m2[nt][x] = now;
+              l[nt][x] *= f;
+#pragma unroll
+              for (int z = 0; z < NG; ++z) {
+                off[nt][z][x] *= f;
+                psum[nt][z][x] *= f;
+              }
+#pragma unroll
+              for (int z = 0; z < 2 * W; ++z) {
+                O[nt][z][x] *= f;
+                O[nt][z][2 + x] *= f;
+              }
+            }
+        }
+        uint32_t vs[2][NG];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint8_t* sp = st + S::kVs + (krow + 8 * x) * (NG * 4);
+          if (NG == 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(sp);
+            vs[x][0] = u.x, vs[x][NG > 1 ? 1 : 0] = u.y, vs[x][NG > 2 ? 2 : 0] = u.z, vs[x][NG > 3 ? 3 : 0] = u.w;
+          } else if (NG == 2) {
+            const uint2 u = *reinterpret_cast<const uint2*>(sp);
+            vs[x][0] = u.x, vs[x][NG > 1 ? 1 : 0] = u.y;
+          } else {
+            vs[x][0] = *reinterpret_cast<const uint32_t*>(sp);
+          }
+        }
+        uint32_t b[NT][NG][PARTS][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+          bool seen[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            seen[x] = !masked || key0 + 8 * (x >> 1) < lim[nt][x & 1];
+            p[x] = ex2_approx(y[nt][x] - m2[nt][x & 1]);
+            if (!seen[x]) p[x] = 0.f;
+            l[nt][x & 1] += p[x];
+          }
+#pragma unroll
+          for (int z = 0; z < NG; ++z) {
+            float ps[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              float add = p[x] * hi_f(vs[x >> 1][z]);
+              ps[x] = p[x] * lo_f(vs[x >> 1][z]);
+              if (!seen[x]) add = ps[x] = 0.f;  // what lies there may be NaN
+              off[nt][z][x & 1] += add;
+            }
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+              const uint32_t u0 = pack2(ps[0], ps[1]), u1 = pack2(ps[2], ps[3]);
+              b[nt][z][part][0] = transpose8(u0);
+              b[nt][z][part][1] = transpose8(u1);
+              if (F32) {
+                ps[0] -= lo_f(u0), ps[1] -= hi_f(u0);
+                ps[2] -= lo_f(u1), ps[3] -= hi_f(u1);
+              } else {
+                const uint32_t one = 0x3f803f80u;
+                mma(psum[nt][z], one, one, one, one, b[nt][z][part][0], b[nt][z][part][1]);
+              }
+            }
+          }
+        }
+        // ---- output: rows channels, columns queries
+        uint32_t vw[4][(W + 1) / 2];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int vr = ((x & 1) ? vrow2 : vrow) + (x >> 1) * 8;
+          const uint8_t* vp = st + S::kV + vr * (D / 2) + vplace * (D / 16);
+          if (W == 4) {
+            const uint2 u = *reinterpret_cast<const uint2*>(vp);
+            vw[x][0] = u.x, vw[x][W / 2 - 1] = u.y;
+          } else {
+            vw[x][0] = *reinterpret_cast<const uint32_t*>(vp);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < W; ++h) {
+          const uint32_t sel = (h & 1) ? 0x7632u : 0x5410u;
+          const uint32_t xx = __byte_perm(vw[0][h >> 1], vw[1][h >> 1], sel);
+          const uint32_t yy = __byte_perm(vw[2][h >> 1], vw[3][h >> 1], sel);
+          uint32_t c0[4], c1[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            c0[n] = codes2<F32>(xx, n);
+            c1[n] = codes2<F32>(yy, n);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int p = PARTS - 1; p >= 0; --p) {
+              const uint32_t b0 = b[nt][h * NG / W][p][0], b1 = b[nt][h * NG / W][p][1];
+              mma(O[nt][2 * h], c0[0], c0[1], c1[0], c1[1], b0, b1);
+              mma(O[nt][2 * h + 1], c0[2], c0[3], c1[2], c1[3], b0, b1);
+            }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    // ---- the CTA leaves the row: the warps' sums are joined
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], o);
+        const int qi = nt * 8 + 2 * tig + x;
+#pragma unroll
+        for (int z = 0; z < NG; ++z) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) off[nt][z][x] += __shfl_xor_sync(0xffffffffu, off[nt][z][x], o);
+        }
+#pragma unroll
+        for (int h = 0; h < W; ++h) {
+          const float add = fmaf(-BIAS, psum[nt][h * NG / W][x], off[nt][h * NG / W][x]);
+          *reinterpret_cast<float4*>(obuf + (warp * NQ + qi) * S::kORow + 32 * h + 4 * grp) =
+              make_float4(O[nt][2 * h][x] + add, O[nt][2 * h][2 + x] + add, O[nt][2 * h + 1][x] + add,
+                          O[nt][2 * h + 1][2 + x] + add);
+        }
+        if (grp == 0) ml[warp * NQ + qi] = make_float2(m2[nt][x], l[nt][x]);
+      }
+    }
+    ok = named_bar_and(1, kWarps * 32, ok);
+    if (!ok) break;
+    const bool whole = t0 == 0 && t1 == tiles;
+    float* part = a.part + (size_t)((chunk * gridDim.x + cta) * 2 + (t0 == 0 ? 1 : 0)) * (kAttnQ * (D + 2));
+    for (int i = threadIdx.x; i < nq * (D / 4); i += kWarps * 32) {
+      const int qi = i / (D / 4), dim = 4 * (i - qi * (D / 4));
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * NQ + qi].x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 e = ml[w * NQ + qi];
+        const float f = e.x == M ? 1.f : ex2_approx(e.x - M);
+        const float4 v = *reinterpret_cast<const float4*>(obuf + (w * NQ + qi) * S::kORow + dim);
+        L += e.y * f;
+        o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+      }
+      if (whole) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const long long at = ((long long)crow * a.R + q0 + qi);
+        if (F32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + dim) =
+              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        } else {
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * D + dim) =
+              make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+        }
+        if (a.lse && dim == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      } else {
+        *reinterpret_cast<float4*>(part + 2 * kAttnQ + qi * D + dim) = o;
+        if (dim == 0) reinterpret_cast<float2*>(part)[qi] = make_float2(M, L);
+      }
+    }
+    named_bar_sync(1, kWarps * 32);  // the buffer is free again
+  }
+}
+
+// Joins the partials of the rows that CTAs shared: block (CTA c, query) works
+// if c is the second CTA of a row. Four warps take every fourth partial.
+template <int D, bool F32>
+__global__ void __launch_bounds__(128) paged_combine_kernel(const AttnArgs a, int grid, int nq_chunk) {
+  __shared__ float4 acc[4][32];
+  __shared__ float2 red[4];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int4 rec = a.split[blockIdx.x];
+  if (rec.x < 0) return;
+  const int qa = blockIdx.y;
+  const int chunk = qa / nq_chunk, qi = qa - chunk * nq_chunk;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = rec.z - rec.y + 1;
+  const size_t stride = kAttnQ * (D + 2);
+  const float* first = a.part + (size_t)(chunk * grid + rec.y) * 2 * stride;
+  // partial k: the first CTA's second slot, then the first slot of each CTA after it
+  auto at = [&](int k) { return first + (k == 0 ? stride : (size_t)k * 2 * stride); };
+  float M = -INFINITY;
+  for (int k = threadIdx.x; k < n; k += 128) M = fmaxf(M, reinterpret_cast<const float2*>(at(k))[qi].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[warp].x = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0].x, red[1].x), fmaxf(red[2].x, red[3].x));
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = warp; k < n; k += 4) {
+    const float* p = at(k);
+    const float2 e = reinterpret_cast<const float2*>(p)[qi];
+    const float f = e.x == M ? 1.f : ex2_approx(e.x - M);
+    L += e.y * f;
+    if (4 * lane < D) {
+      const float4 v = *reinterpret_cast<const float4*>(p + 2 * kAttnQ + qi * D + 4 * lane);
+      o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+    }
+  }
+  acc[warp][lane] = o;
+  if (lane == 0) red[warp].y = L;
+  __syncthreads();
+  if (warp == 0 && 4 * lane < D) {
+    L = (red[0].y + red[1].y) + (red[2].y + red[3].y);
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float4 v = acc[w][lane];
+      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const long long q = (long long)(a.row0 + rec.x) * a.R + qa;
+    if (F32)
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + q * D + 4 * lane) =
+          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    else
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + q * D + 4 * lane) =
+          make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+    if (a.lse && lane == 0) a.lse[q] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
+}
+
+template <class K, class... A>
+int launch_pdl(K k, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, k, args...));
+}
+
+template <int D, int NG, int NT, bool F32>
+int run(AttnArgs a, cudaStream_t st) {
+  using S = Smem<D, NG, NT>;
+  auto k = paged_attn_kernel<D, NG, NT, F32>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
+    return KV_ERR_CUDA;
+  const int chunks = (a.R + S::NQ - 1) / S::NQ;
+  const int per_sm = NT == 1 && !F32 ? kAttnCtasPerSm : 2;
+  const int grid = max(1, sm_count() * per_sm / chunks);
+  const int all = a.rows.n_rows;
+  for (int r0 = 0; r0 < all; r0 += kAttnRows) {
+    a.row0 = r0;
+    a.n_rows = min(kAttnRows, all - r0);
+    int rc = launch_pdl(k, dim3(grid, chunks), kThreads, S::kBytes, st, a);
+    if (rc) return rc;
+    rc = launch_pdl(paged_combine_kernel<D, F32>, dim3(grid, a.R), 128, 0, st, a, grid, S::NQ);
+    if (rc) return rc;
+  }
+  return KV_OK;
+}
+
+template <int D, int NG>
+int run_as(const AttnArgs& a, bool f32, cudaStream_t st) {
+  if (f32) return run<D, NG, 1, true>(a, st);
+  return a.R <= 8 ? run<D, NG, 1, false>(a, st) : run<D, NG, 2, false>(a, st);
+}
+
+}  // namespace
+
+int launch_paged_attn(const kv_paged_shape& sh, const PageGeom& g, const SeqRows& rows, const PagedCache& c,
+                      uint8_t* ws, int n_q, const void* q, void* out, float* lse, cudaStream_t st) {
+  AttnArgs a = {};
+  a.g = g;
+  a.rows = rows;
+  a.c = c;
+  a.n_q = n_q;
+  a.group = sh.group;
+  a.R = n_q * sh.group;
+  a.scale2 = 1.4426950408889634f / sqrtf((float)sh.head_dim);
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  const PagedWs w = paged_ws_layout(sh);
+  a.split = reinterpret_cast<int4*>(ws + w.att_base);
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.limit_ns = wait_limit_ns();
+  const bool f32 = sh.dtype == KV_F32;
+  if (g.d == 64) return g.G == 1 ? run_as<64, 1>(a, f32, st) : run_as<64, 2>(a, f32, st);
+  return g.G == 1 ? run_as<128, 1>(a, f32, st) : g.G == 2 ? run_as<128, 2>(a, f32, st) : run_as<128, 4>(a, f32, st);
+}
+
+}  // namespace kvc

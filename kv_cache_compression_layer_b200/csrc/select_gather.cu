@@ -306,14 +306,21 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-int launch_select_gather(const kv_shape& sh, const RowMap& m, const float* s_hat, const void* K, const void* V,
-                         const int32_t* b, const int64_t* slot_off, int32_t* idx, void* Kc, void* Vc, int nseg,
-                         cudaStream_t st) {
+int launch_select(const kv_shape& sh, const RowMap& m, const float* s_hat, const int32_t* b,
+                  const int64_t* slot_off, int32_t* idx, int nseg, cudaStream_t st) {
   // a per-device setting: made on every launch (cheap), for whichever device is current
   const size_t smem = sel_smem_bytes(m, nseg);
   if (cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return KV_ERR_CUDA;
   select_kernel<<<m.n_rows, kSelThreads, smem, st>>>(m, sh.w, nseg, s_hat, b, slot_off, idx);
+  return cuda_status(cudaGetLastError());
+}
+
+int launch_select_gather(const kv_shape& sh, const RowMap& m, const float* s_hat, const void* K, const void* V,
+                         const int32_t* b, const int64_t* slot_off, int32_t* idx, void* Kc, void* Vc, int nseg,
+                         cudaStream_t st) {
+  const int rc = launch_select(sh, m, s_hat, b, slot_off, idx, nseg, st);
+  if (rc) return rc;
   const int esz = sh.dtype == KV_BF16 ? 2 : 4;
   const int row_bytes = sh.head_dim * esz;
   gather_kernel<<<sm_count() * 8, 256, 0, st>>>(m, row_bytes, slot_off, b, idx, static_cast<const uint8_t*>(K),

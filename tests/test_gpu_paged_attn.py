@@ -1,0 +1,191 @@
+"""kv_paged_attn against a softmax in float64 over the values held, within
+bounds derived from its arithmetic (tests/_paged.py, Model.attention)."""
+import numpy as np
+import pytest
+import torch
+
+import kv_cache_compression_layer_b200 as kv
+from tests import _paged as pg
+
+pytestmark = pytest.mark.gpu
+
+
+def queries(rng, m, rows, R, dtype, dev):
+    """Queries near one of their row's keys."""
+    d = m.sh.head_dim
+    q = 0.3 * rng.normal(size=(len(rows), R, d))
+    for i, r in enumerate(rows):
+        if m.len[r]:
+            q[i] += 0.5 * m.K[r][rng.integers(0, m.len[r], R), 0]
+    return pg.up(np.nan_to_num(q), dtype, dev)
+
+
+def attend(cache, m, rng, seqs, n_q=1, layers=None, rows_at=None):
+    rows = m.call_rows(seqs, layers)
+    R = n_q * m.sh.group
+    q = queries(rng, m, rows, R, m.sh.dtype, cache.device)
+    out, lse = torch.full_like(q, 3.0), torch.full(q.shape[:2], 3.0, device=cache.device)
+    cache.attend(seqs, q, out, lse=lse, n_q=n_q, layers=layers)
+    assert cache.read_status() == m.status
+    m.check_attention(q, out, lse, seqs, n_q, layers, rows_at)
+    return q, out, lse
+
+
+CASES = [  # d, group size, page, type, g, n_q
+    (128, 64, 64, kv.KV_BF16, 8, 1), (128, 32, 16, kv.KV_BF16, 7, 1), (128, 128, 128, kv.KV_BF16, 1, 1),
+    (64, 64, 32, kv.KV_BF16, 5, 1), (64, 32, 64, kv.KV_BF16, 16, 1), (128, 64, 64, kv.KV_BF16, 8, 4),
+    (128, 32, 32, kv.KV_BF16, 3, 5), (128, 128, 16, kv.KV_BF16, 1, 64), (64, 64, 128, kv.KV_BF16, 7, 9),
+    (64, 32, 128, kv.KV_BF16, 4, 2), (128, 64, 128, kv.KV_F32, 8, 1), (128, 32, 64, kv.KV_F32, 1, 1),
+    (64, 32, 16, kv.KV_F32, 3, 3), (64, 64, 64, kv.KV_F32, 16, 1), (128, 128, 32, kv.KV_F32, 5, 8)]
+
+
+@pytest.mark.parametrize("d,qg,page,dtype,g,n_q", CASES)
+def test_ragged_rows(d, qg, page, dtype, g, n_q):
+    """Rows of 0, 1, a few and several hundred tokens, odd ends of pages and tiles."""
+    rng = np.random.default_rng(d + qg + page + g + n_q)
+    cache, m = pg.make(n_seqs=3, n_layers=2, heads=2, group=g, d=d, qg=qg, page=page, dtype=dtype,
+                       max_pages=-(-700 // page))
+    pg.fill(cache, m, [0, 1, 2, 15, 16, 17, 63, 64, 65, 129, 333, 700], rng)
+    attend(cache, m, rng, [0, 1, 2], n_q)
+    attend(cache, m, rng, [2, 0], n_q, layers=(1, 1))
+
+
+@pytest.mark.parametrize("dtype", [kv.KV_BF16, kv.KV_F32])
+@pytest.mark.parametrize("n", [1, 64, 4097, 32768])
+def test_one_row(n, dtype):
+    """One row over all CTAs: their partials are joined."""
+    rng = np.random.default_rng(n)
+    cache, m = pg.make(n_seqs=1, n_layers=1, heads=1, group=8, dtype=dtype, max_pages=512)
+    pg.fill(cache, m, [n], rng)
+    attend(cache, m, rng, [0])
+    attend(cache, m, rng, [0], n_q=3)
+
+
+def test_many_rows():
+    """More rows than one launch takes, most of them short, some empty."""
+    rng = np.random.default_rng(1)
+    cache, m = pg.make(n_seqs=40, n_layers=10, heads=6, group=2, d=64, qg=32, page=16, max_pages=6)
+    pg.fill(cache, m, rng.integers(0, 80, m.rows), rng)
+    assert m.rows > 2 * 1024
+    attend(cache, m, rng, list(range(40)), rows_at=set(range(0, m.rows, 7)))
+
+
+def test_pages_in_any_place_and_repeatable():
+    """The same tokens on other pages give the same bits; so does the same call again."""
+    rng = np.random.default_rng(2)
+    cache, m = pg.make(n_seqs=2, n_layers=2, heads=2, group=7, page=32, max_pages=24, n_pages=400)
+    pg.fill(cache, m, rng.integers(1, 600, m.rows), rng)
+    q, out, lse = attend(cache, m, rng, [0, 1])
+    out2, lse2 = torch.empty_like(out), torch.empty_like(lse)
+    cache.attend([0, 1], q, out2, lse=lse2)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    perm = torch.randperm(400, generator=torch.Generator().manual_seed(0)).to(cache.device)
+    table = cache.table.clone()
+    moved = torch.zeros_like(cache.pages)
+    moved[perm] = cache.pages
+    other = kv.PagedCache(cache.shape, pages=moved, table=perm[table.long()].to(torch.int32), lens=cache.lens.clone())
+    other.attend([0, 1], q, out2, lse=lse2)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+def test_what_lies_behind_a_row_is_not_read():
+    """NaN scales behind the last token, in the part of a page that a row does not fill, reach no output; a NaN token
+    does, and only those queries that see it."""
+    rng = np.random.default_rng(4)
+    for dtype in (kv.KV_BF16, kv.KV_F32):
+        cache, m = pg.make(n_seqs=1, n_layers=1, heads=3, group=2, dtype=dtype, max_pages=4)
+        cache.pages.fill_(0xff)
+        pg.fill(cache, m, [5, 100, 64], rng)
+        attend(cache, m, rng, [0])
+        attend(cache, m, rng, [0], n_q=4)
+        K, V = pg.tokens(rng, 9, 128, dtype)
+        V[5, 7] = np.nan  # the second row's last token
+        rows = m.call_rows([0])
+        Kr, Vr = K.reshape(3, 3, 128), V.reshape(3, 3, 128)
+        m.append(rows, Kr, Vr)
+        cache.append([0], pg.up(Kr, dtype, cache.device), pg.up(Vr, dtype, cache.device))
+        q = queries(rng, m, rows, 4, dtype, cache.device)
+        out = torch.empty_like(q)
+        cache.attend([0], q, out, n_q=2)
+        bad = torch.isnan(out.float()).cpu()
+        assert not bad[0].any() and not bad[2].any()
+        # the first query does not see it; the second has it in the group of channels that holds the NaN
+        assert not bad[1, :2].any() and not bad[1, :, 64:].any() and bad[1, 2:, :64].all()
+        out3 = torch.empty(3, 6, 128, dtype=q.dtype, device=cache.device)
+        cache.attend([0], queries(rng, m, rows, 6, dtype, cache.device), out3, n_q=3)
+        bad = torch.isnan(out3.float()).cpu()
+        assert not bad[1, :4].any() and bad[1, 4:, :64].all()
+
+
+def test_large_logits():
+    """Queries that leave all of the weight on one key, and keys in falling and rising order of their logits."""
+    rng = np.random.default_rng(9)
+    cache, m = pg.make(n_seqs=1, n_layers=1, heads=2, group=4, qg=128, max_pages=8)
+    n = 400
+    K, V = pg.tokens(rng, 2 * n, 128, 1)
+    K = pg.bf16(K * np.concatenate([np.linspace(0.1, 4, n), np.linspace(4, 0.1, n)])[:, None])
+    m.append([0, 1], K.reshape(2, n, 128), V.reshape(2, n, 128))
+    cache.append([0], pg.up(K, 1, cache.device), pg.up(V, 1, cache.device))
+    q = queries(rng, m, [0, 1], 4, 1, cache.device) * 8
+    out, lse = torch.empty_like(q), torch.empty(2, 4, device=cache.device)
+    cache.attend([0], q, out, lse=lse)
+    m.check_attention(q, out, lse, [0], 1)
+
+
+def test_another_stream_and_graph():
+    """A captured step (append, attention) replayed on another stream equals the steps one by one."""
+    rng = np.random.default_rng(10)
+    cache, m = pg.make(n_seqs=2, n_layers=2, heads=2, group=4, page=16, max_pages=8)
+    twin, m2 = pg.make(n_seqs=2, n_layers=2, heads=2, group=4, page=16, max_pages=8)
+    counts = rng.integers(0, 40, m.rows)
+    pg.fill(cache, m, counts, np.random.default_rng(0))
+    pg.fill(twin, m2, counts, np.random.default_rng(0))
+    dev = cache.device
+    steps = [(pg.tokens(rng, m.rows, 128, 1), 0.5 * rng.normal(size=(m.rows, 4, 128))) for _ in range(6)]
+    k, v = (torch.zeros(m.rows, 128, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    q = torch.zeros(m.rows, 4, 128, dtype=torch.bfloat16, device=dev)
+    out = torch.zeros_like(q)
+    st = torch.cuda.Stream(dev)
+    st.wait_stream(torch.cuda.current_stream(dev))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        cache.append([0, 1], k, v)
+        cache.attend([0, 1], q, out)
+    for (K, V), Q in steps:
+        with torch.cuda.stream(st):
+            k.copy_(pg.up(K, 1, dev)), v.copy_(pg.up(V, 1, dev)), q.copy_(pg.up(Q, 1, dev))
+            graph.replay()
+        m2.append(m2.call_rows([0, 1]), K[:, None], V[:, None])
+        twin.append([0, 1], pg.up(K, 1, dev), pg.up(V, 1, dev))
+        want = twin.attend([0, 1], pg.up(Q, 1, dev))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    m2.check(cache)
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """With no time to wait the call gives up with a status; the next one is sound."""
+    rng = np.random.default_rng(12)
+    cache, m = pg.make(n_seqs=1, n_layers=2, heads=2, max_pages=32)
+    pg.fill(cache, m, rng.integers(200, 2000, m.rows), rng)
+    q = queries(rng, m, m.call_rows([0]), 3, 1, cache.device)
+    prev = kv.kv_set_wait_limit_ns(0)
+    try:
+        cache.attend([0], q)
+        assert cache.read_status() == kv.KV_DEV_TIMEOUT
+    finally:
+        kv.kv_set_wait_limit_ns(prev)
+    cache.status.zero_()
+    attend(cache, m, rng, [0])
+
+
+def test_bad_page_numbers_are_reported():
+    rng = np.random.default_rng(13)
+    cache, m = pg.make(n_seqs=2, n_layers=1, heads=1, group=2, max_pages=4)
+    pg.fill(cache, m, [200, 200], rng)
+    cache.table[0, 1] = -1
+    cache.table[0, 2] = cache.shape.n_pages
+    q = queries(rng, m, [0, 1], 2, 1, cache.device)
+    out = cache.attend([0, 1], q)
+    assert cache.read_status() == kv.KV_DEV_BOUNDS
+    m.check_attention(q, out, None, [0, 1], 1, rows_at={1})
