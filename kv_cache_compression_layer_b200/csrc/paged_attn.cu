@@ -2,23 +2,31 @@
 // cache (formats in include/kvcomp_paged.h).
 //
 // What bounds it: the codes and scales are read once, d + 8 G bytes a token
-// (144 at d = 128 and groups of 64); the arithmetic to unpack them is near the
-// SMs' issue rate at that bandwidth, so the inner loop is kept to about an
-// instruction a code.
+// (144 at d = 128 and groups of 64); to unpack them at that bandwidth takes
+// most of the SMs' issue slots, and twice its share of the logic pipe, which
+// takes an instruction every other cycle.
 //
-// Products. Codes go to the tensor cores as bf16 without a conversion: bits
-// 0-3 of a 16-bit half or-ed into 0x4300 are the bf16 number 128 + c exactly.
-// With a group's step s and base m taken out of the sums,
-//   q.k = sum_g s_g (q.(128 + c))_g + (m_g - 128 s_g) (sum of q over g),
-//   sum_j p_j v_j = sum_j p'_j (128 + c_j) - 128 sum_j p'_j + sum_j p_j m_j,
-// p'_j = p_j s_j rounded to bf16 (its sum is that of the rounded numbers, so
-// the rounding is the only error: at most 2^-8 of a term). fp32 caches take c itself
-// (one subtraction a pair) and split q and p' into three bf16 parts each, which
-// together hold their 24 bits. Both products have the cache as the 16-row
-// operand (mma.sync m16n8k16: keys x queries, then channels x queries), so up
-// to 8 queries cost no padding; a warp's fragments are one 16-byte load of K
-// codes a key and 8-byte loads of V codes, free of bank conflicts by the
-// page's order of words and the order in which a tile's keys take the rows.
+// Products. A pair of codes becomes two fp16 with one logic instruction and
+// one addition: bits 0-3 of a 16-bit half or-ed into 0x6400 are the number
+// 1024 + c, bits 4-7 or-ed into 0x5400 the number 64 + c; less 1032 or 72 they
+// are c - 8, exactly. With a group's step s and base m taken out of the sums,
+// and b = m + 8 s,
+//   q.k = sum_g s_g (q.(c - 8))_g + b_g (sum of q over g),
+//   sum_j p_j v_j = sum_j p'_j (c_j - 8) + sum_j p_j b_j,   p'_j = p_j s_j.
+// (Keeping an offset in the codes and subtracting it from the sums would save
+// the additions, but the tensor cores drop what lies below a running sum's last
+// bit: with 256 the outputs of 6400 keys were 0.7 % off.)
+// q is scaled by a power of two per query that brings its largest channel to
+// [256, 512), so a bf16 q is held exactly but for channels 2^22 below that; p'
+// is rounded to fp16 (2^-11 of a term) and scaled by a power of two that keeps
+// a row's largest step below 2^6 (p stays below 2^8), which follows a larger
+// step as the softmax's maximum follows a larger logit. For fp32 q and p' are
+// two fp16 each (22 bits).
+// Both products have the cache as the 16-row operand (mma.sync m16n8k16: keys x
+// queries, then channels x queries), so up to 8 queries cost no padding; a
+// warp's fragments are one 16-byte load of K codes a key and 8-byte loads of V
+// codes, free of bank conflicts by the page's order of words and the order in
+// which a tile's keys take the rows.
 //
 // Work. Rows are cut into tiles of 64 tokens; a row costs its tiles plus one.
 // The CTAs (up to three per SM) take equal shares of the total, contiguous
@@ -28,6 +36,11 @@
 // joined when the CTA leaves the row. A row that several CTAs share leaves
 // partials, joined by paged_combine_kernel in CTA order. Every sum has a fixed
 // order.
+#include <cuda_fp16.h>
+
+#include <climits>
+#include <type_traits>
+
 #include "paged_common.cuh"
 
 namespace kvc {
@@ -69,30 +82,57 @@ struct Smem {
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+// Two fp16 of a and b (lo in the low half), and what their rounding left of them.
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void rest2(uint32_t u, float& lo, float& hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+  lo -= f.x;
+  hi -= f.y;
+}
+__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ uint32_t add2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
 
-// Nibble pair n of x (bits 4 n and 16 + 4 n) as two bf16: 128 + c, or c itself.
-template <bool PLAIN>
-__device__ __forceinline__ uint32_t codes2(uint32_t x, int n) {
-  const uint32_t r = ((x >> (4 * n)) & 0x000f000fu) | 0x43004300u;
-  if (!PLAIN) return r;
-  const uint32_t b = 0x43004300u;
-  const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&r), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&y);
+// The four nibble pairs of x (bits 4 n and 16 + 4 n) as two fp16 each: c - 8.
+__device__ __forceinline__ void codes8(uint32_t x, uint32_t (&c)[4]) {
+  const uint32_t y = x >> 8;
+  c[0] = add2((x & 0x000f000fu) | 0x64006400u, 0xe408e408u);
+  c[1] = add2((x & 0x00f000f0u) | 0x54005400u, 0xd480d480u);
+  c[2] = add2((y & 0x000f000fu) | 0x64006400u, 0xe408e408u);
+  c[3] = add2((y & 0x00f000f0u) | 0x54005400u, 0xd480d480u);
+}
+// The NG scales of a token.
+template <int NG>
+__device__ __forceinline__ void load_scales(const uint8_t* p, uint32_t (&s)[NG]) {
+  if constexpr (NG == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    s[0] = u.x, s[1] = u.y, s[2] = u.z, s[3] = u.w;
+  } else if constexpr (NG == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    s[0] = u.x, s[1] = u.y;
+  } else {
+    s[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -108,8 +148,7 @@ __device__ __forceinline__ int cta_count(int cost, int grid) { return max(1, min
 template <int D, int NG, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2) paged_attn_kernel(const AttnArgs a) {
   using S = Smem<D, NG, NT>;
-  constexpr int W = D / 32, NQ = S::NQ, PARTS = F32 ? 3 : 1;
-  constexpr float BIAS = F32 ? 0.f : 128.f;
+  constexpr int W = D / 32, NQ = S::NQ, PARTS = F32 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   float* obuf = reinterpret_cast<float*>(smem + S::kObuf);
   float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
@@ -256,52 +295,66 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     const int q0 = chunk * NQ, nq = min(NQ, a.R - q0);
     const int len = tiles > 0 ? a.c.len[table_row(a.rows, crow)] : 0;
 
-    // query fragments and their sums by group
+    // query fragments, their sums by group, and what turns a sum into a logit in log2 units
     uint32_t qf[NT][PARTS][W][4];
-    float qsum[NT][NG][2];
+    float qsum[NT][NG][2], unit[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int qi = nt * 8 + grp;
-      float sum[NG];
-#pragma unroll
-      for (int x = 0; x < NG; ++x) sum[x] = 0.f;
+      float x[W][8], top = 0.f, sum[NG];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        float x[8];
         const long long at = ((long long)crow * a.R + q0 + qi) * D + 32 * w + 8 * tig;
         if (qi < nq) {
           if (F32) {
             const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
             const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 4);
-            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+            x[w][0] = u.x, x[w][1] = u.y, x[w][2] = u.z, x[w][3] = u.w;
+            x[w][4] = v.x, x[w][5] = v.y, x[w][6] = v.z, x[w][7] = v.w;
           } else {
             const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
-            x[0] = lo_f(u.x), x[1] = hi_f(u.x), x[2] = lo_f(u.y), x[3] = hi_f(u.y);
-            x[4] = lo_f(u.z), x[5] = hi_f(u.z), x[6] = lo_f(u.w), x[7] = hi_f(u.w);
+            x[w][0] = lo_f(u.x), x[w][1] = hi_f(u.x), x[w][2] = lo_f(u.y), x[w][3] = hi_f(u.y);
+            x[w][4] = lo_f(u.z), x[w][5] = hi_f(u.z), x[w][6] = lo_f(u.w), x[w][7] = hi_f(u.w);
           }
         } else {
 #pragma unroll
-          for (int n = 0; n < 8; ++n) x[n] = 0.f;
+          for (int n = 0; n < 8; ++n) x[w][n] = 0.f;
         }
 #pragma unroll
-        for (int n = 0; n < 8; ++n) sum[w * NG / W] += x[n];
+        for (int n = 0; n < 8; ++n) top = fmaxf(top, fabsf(x[w][n]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = max(-100, (int)(__float_as_uint(top) >> 23) - 127);  // 2^e <= top < 2^(e + 1)
+      const float up = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+      const float down = a.scale2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+#pragma unroll
+      for (int z = 0; z < NG; ++z) sum[z] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          x[w][n] *= up;
+          sum[w * NG / W] += x[w][n];
+        }
 #pragma unroll
         for (int p = 0; p < PARTS; ++p)
 #pragma unroll
           for (int n = 0; n < 4; ++n) {  // a code pair holds channels n and n + 4
-            qf[nt][p][w][n] = pack2(x[n], x[n + 4]);
-            if (F32) {
-              x[n] -= lo_f(qf[nt][p][w][n]);
-              x[n + 4] -= hi_f(qf[nt][p][w][n]);
-            }
+            qf[nt][p][w][n] = pack2(x[w][n], x[w][n + 4]);
+            rest2(qf[nt][p][w][n], x[w][n], x[w][n + 4]);
           }
       }
 #pragma unroll
-      for (int x = 0; x < NG; ++x) {
-        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
-        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
-        qsum[nt][x][0] = __shfl_sync(0xffffffffu, sum[x], (2 * tig) * 4);
-        qsum[nt][x][1] = __shfl_sync(0xffffffffu, sum[x], (2 * tig + 1) * 4);
+      for (int z = 0; z < NG; ++z) {
+        sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 1);
+        sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 2);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {  // lane 4 r holds those of query r; this lane's columns are queries 2 tig + c
+#pragma unroll
+        for (int z = 0; z < NG; ++z) qsum[nt][z][c] = __shfl_sync(0xffffffffu, sum[z], (2 * tig + c) * 4);
+        unit[nt][c] = __shfl_sync(0xffffffffu, down, (2 * tig + c) * 4);
       }
     }
     // keys that this lane's queries see
@@ -315,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         lim[nt][x] = qi < nq ? lim_min + (q0 + qi) / a.group : len;
       }
 
-    float O[NT][2 * W][4], psum[NT][NG][4], off[NT][NG][2], m2[NT][2], l[NT][2];
+    float O[NT][2 * W][4], off[NT][NG][2], m2[NT][2], thr[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -323,48 +376,35 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
 #pragma unroll
         for (int y = 0; y < 4; ++y) O[nt][x][y] = 0.f;
 #pragma unroll
-      for (int x = 0; x < NG; ++x) {
-#pragma unroll
-        for (int y = 0; y < 4; ++y) psum[nt][x][y] = 0.f;
-        off[nt][x][0] = off[nt][x][1] = 0.f;
-      }
-      m2[nt][0] = m2[nt][1] = -INFINITY;
+      for (int x = 0; x < NG; ++x) off[nt][x][0] = off[nt][x][1] = 0.f;
+      m2[nt][0] = m2[nt][1] = thr[nt][0] = thr[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
+    float om = 1.f, s_top = -1.f;  // scale of p', and the largest step that it is made for
 
-    for (int t = t0; ok && t < t1; ++t, ++it) {
-      const int s = it % kStages;
-      ok = wait_bounded(&full[s], (it / kStages) & 1, guard);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint8_t* st = smem + s * S::kStage;
-      const int tok0 = t * kTile + warp * 16;
-      const bool some = tok0 < len;                // the warp's tokens hold keys
-      const bool masked = tok0 + 16 > lim_min;     // some of them are hidden from some query
-      const int key0 = tok0 + krow - warp * 16;    // keys of matrix rows grp and grp + 8: key0, key0 + 8
-      if (some) {
-        // ---- logits: rows keys, columns queries
+    // 16 keys from each of two stages; MASKED: some are hidden from some query, or (key >= none) not there.
+    auto keys32 = [&](auto mk, const uint8_t* st0, const uint8_t* st1, int key0, int key1) {
+      constexpr bool MASKED = decltype(mk)::value;
+      constexpr int U = 2;
+      const uint8_t* sts[U] = {st0, st1};
+      const int keys[U] = {key0, key1};  // of matrix row grp; row grp + 8 is 8 further
+      // ---- logits: rows keys, columns queries
+      float y[U][NT][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint8_t* st = sts[u];
         uint32_t kw[2][W], ks[2][NG];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const uint8_t* kp = st + (krow + 8 * x) * (D / 2) + tig * (D / 8);
-          if (W == 4) {
-            const uint4 u = *reinterpret_cast<const uint4*>(kp);
-            kw[x][0] = u.x, kw[x][1] = u.y, kw[x][W - 2] = u.z, kw[x][W - 1] = u.w;
+          if constexpr (W == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(kp);
+            kw[x][0] = v.x, kw[x][1] = v.y, kw[x][2] = v.z, kw[x][3] = v.w;
           } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(kp);
-            kw[x][0] = u.x, kw[x][1] = u.y;
+            const uint2 v = *reinterpret_cast<const uint2*>(kp);
+            kw[x][0] = v.x, kw[x][1] = v.y;
           }
-          const uint8_t* sp = st + S::kKs + (krow + 8 * x) * (NG * 4);
-          if (NG == 4) {
-            const uint4 u = *reinterpret_cast<const uint4*>(sp);
-            ks[x][0] = u.x, ks[x][NG > 1 ? 1 : 0] = u.y, ks[x][NG > 2 ? 2 : 0] = u.z, ks[x][NG > 3 ? 3 : 0] = u.w;
-          } else if (NG == 2) {
-            const uint2 u = *reinterpret_cast<const uint2*>(sp);
-            ks[x][0] = u.x, ks[x][NG > 1 ? 1 : 0] = u.y;
-          } else {
-            ks[x][0] = *reinterpret_cast<const uint32_t*>(sp);
-          }
+          load_scales<NG>(st + S::kKs + (krow + 8 * x) * (NG * 4), ks[x]);
         }
         float acc[NT][NG][4];
 #pragma unroll
@@ -372,15 +412,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
 #pragma unroll
           for (int x = 0; x < NG; ++x)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) acc[nt][x][y] = 0.f;
+            for (int z = 0; z < 4; ++z) acc[nt][x][z] = 0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           uint32_t c0[4], c1[4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            c0[n] = codes2<F32>(kw[0][w], n);
-            c1[n] = codes2<F32>(kw[1][w], n);
-          }
+          codes8(kw[0][w], c0);
+          codes8(kw[1][w], c1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -389,100 +426,126 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
               mma(acc[nt][w * NG / W], c0[2], c1[2], c0[3], c1[3], qf[nt][p][w][2], qf[nt][p][w][3]);
             }
         }
-        float y[NT][4];
-        bool grow = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int x = 0; x < NG; ++x)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) y[nt][x] = 0.f;
+          for (int z = 0; z < 2; ++z) {
+            const float sc = lo_f(ks[z][x]), ad = fmaf(8.f, sc, hi_f(ks[z][x]));
 #pragma unroll
-          for (int x = 0; x < NG; ++x)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const float sc = lo_f(ks[z][x]), ad = fmaf(-BIAS, sc, hi_f(ks[z][x]));
-              y[nt][2 * z] = fmaf(sc, acc[nt][x][2 * z], fmaf(ad, qsum[nt][x][0], y[nt][2 * z]));
-              y[nt][2 * z + 1] = fmaf(sc, acc[nt][x][2 * z + 1], fmaf(ad, qsum[nt][x][1], y[nt][2 * z + 1]));
-            }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            y[nt][x] *= a.scale2;
-            if (masked && key0 + 8 * (x >> 1) >= lim[nt][x & 1]) y[nt][x] = -INFINITY;
-            grow |= y[nt][x] > m2[nt][x & 1] + kGrow;
+              for (int c = 0; c < 2; ++c) {
+                const float add = x == 0 ? ad * qsum[nt][x][c] : fmaf(ad, qsum[nt][x][c], y[u][nt][2 * z + c]);
+                y[u][nt][2 * z + c] = fmaf(sc, acc[nt][x][2 * z + c], add);
+              }
           }
-        }
-        // ---- softmax: the running maximum follows only when a logit passes it by far
-        if (__any_sync(0xffffffffu, grow)) {
+        if constexpr (MASKED) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              float mx = fmaxf(y[nt][x], y[nt][2 + x]);
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              const float now = fmaxf(m2[nt][x], mx);
-              const float f = now == m2[nt][x] ? 1.f : ex2_approx(m2[nt][x] - now);
-              m2[nt][x] = now;
-              l[nt][x] *= f;
-#pragma unroll
-              for (int z = 0; z < NG; ++z) {
-                off[nt][z][x] *= f;
-                psum[nt][z][x] *= f;
-              }
-#pragma unroll
-              for (int z = 0; z < 2 * W; ++z) {
-                O[nt][z][x] *= f;
-                O[nt][z][2 + x] *= f;
-              }
-            }
+            for (int x = 0; x < 4; ++x)
+              if (keys[u] + 8 * (x >> 1) >= lim[nt][x & 1]) y[u][nt][x] = -INFINITY;
         }
-        uint32_t vs[2][NG];
+      }
+      uint32_t vs[U][2][NG];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const uint8_t* sp = st + S::kVs + (krow + 8 * x) * (NG * 4);
-          if (NG == 4) {
-            const uint4 u = *reinterpret_cast<const uint4*>(sp);
-            vs[x][0] = u.x, vs[x][NG > 1 ? 1 : 0] = u.y, vs[x][NG > 2 ? 2 : 0] = u.z, vs[x][NG > 3 ? 3 : 0] = u.w;
-          } else if (NG == 2) {
-            const uint2 u = *reinterpret_cast<const uint2*>(sp);
-            vs[x][0] = u.x, vs[x][NG > 1 ? 1 : 0] = u.y;
-          } else {
-            vs[x][0] = *reinterpret_cast<const uint32_t*>(sp);
+          load_scales<NG>(sts[u] + S::kVs + (krow + 8 * x) * (NG * 4), vs[u][x]);
+          if constexpr (MASKED) {
+            if (keys[u] + 8 * x >= len) {
+#pragma unroll
+              for (int z = 0; z < NG; ++z) vs[u][x][z] = 0;  // what lies there may be NaN
+            }
           }
         }
+      // ---- softmax: the running maximum follows only when a logit passes it by far
+      bool grow = false;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) grow |= y[u][nt][x] > thr[nt][x & 1];
+      float s_max = 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int z = 0; z < NG; ++z) s_max = fmaxf(s_max, lo_f(vs[u][x][z]));
+      grow |= s_max > s_top;
+      if (__any_sync(0xffffffffu, grow)) {
+        float fo = 1.f;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) s_max = fmaxf(s_max, __shfl_xor_sync(0xffffffffu, s_max, o));
+        if (s_max > s_top) {
+          // 2^e <= s_max < 2^(e + 1): p' is scaled by 2^(5 - e), at most 2^100; a step of 0 leaves the choice open
+          const int e = max(-95, (int)(__float_as_uint(s_max) >> 23) - 127);
+          const float now = __uint_as_float((uint32_t)(127 + 5 - e) << 23);
+          s_top = s_max == 0.f ? 0.f : __uint_as_float((uint32_t)(127 + e + 1) << 23);
+          fo = now / om;
+          om = now;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float mx = fmaxf(fmaxf(y[0][nt][x], y[0][nt][2 + x]), fmaxf(y[1][nt][x], y[1][nt][2 + x]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float now = fmaxf(m2[nt][x], mx * unit[nt][x]);
+            const float f = now == m2[nt][x] ? 1.f : ex2_approx(m2[nt][x] - now), g2 = f * fo;
+            m2[nt][x] = now;
+            thr[nt][x] = (now + kGrow) / unit[nt][x];
+            l[nt][x] *= f;
+#pragma unroll
+            for (int z = 0; z < NG; ++z) off[nt][z][x] *= f;
+#pragma unroll
+            for (int z = 0; z < 2 * W; ++z) {
+              O[nt][z][x] *= g2;
+              O[nt][z][2 + x] *= g2;
+            }
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint8_t* st = sts[u];
         uint32_t b[NT][NG][PARTS][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
+          float p[4], po[4];
           bool seen[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            seen[x] = !masked || key0 + 8 * (x >> 1) < lim[nt][x & 1];
-            p[x] = ex2_approx(y[nt][x] - m2[nt][x & 1]);
+            seen[x] = !MASKED || keys[u] + 8 * (x >> 1) < lim[nt][x & 1];
+            p[x] = ex2_approx(fmaf(y[u][nt][x], unit[nt][x & 1], -m2[nt][x & 1]));
             if (!seen[x]) p[x] = 0.f;
             l[nt][x & 1] += p[x];
+            po[x] = p[x] * om;
           }
 #pragma unroll
           for (int z = 0; z < NG; ++z) {
             float ps[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              float add = p[x] * hi_f(vs[x >> 1][z]);
-              ps[x] = p[x] * lo_f(vs[x >> 1][z]);
-              if (!seen[x]) add = ps[x] = 0.f;  // what lies there may be NaN
-              off[nt][z][x & 1] += add;
+              const float sc = lo_f(vs[u][x >> 1][z]), ba = fmaf(8.f, sc, hi_f(vs[u][x >> 1][z]));
+              ps[x] = po[x] * sc;
+              if constexpr (MASKED) {
+                off[nt][z][x & 1] += seen[x] ? p[x] * ba : 0.f;  // a token that another query sees may be NaN
+                if (!seen[x]) ps[x] = 0.f;
+              } else {
+                off[nt][z][x & 1] = fmaf(p[x], ba, off[nt][z][x & 1]);
+              }
             }
 #pragma unroll
             for (int part = 0; part < PARTS; ++part) {
               const uint32_t u0 = pack2(ps[0], ps[1]), u1 = pack2(ps[2], ps[3]);
               b[nt][z][part][0] = transpose8(u0);
               b[nt][z][part][1] = transpose8(u1);
-              if (F32) {
-                ps[0] -= lo_f(u0), ps[1] -= hi_f(u0);
-                ps[2] -= lo_f(u1), ps[3] -= hi_f(u1);
-              } else {
-                const uint32_t one = 0x3f803f80u;
-                mma(psum[nt][z], one, one, one, one, b[nt][z][part][0], b[nt][z][part][1]);
-              }
+              rest2(u0, ps[0], ps[1]);
+              rest2(u1, ps[2], ps[3]);
             }
           }
         }
@@ -492,9 +555,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         for (int x = 0; x < 4; ++x) {
           const int vr = ((x & 1) ? vrow2 : vrow) + (x >> 1) * 8;
           const uint8_t* vp = st + S::kV + vr * (D / 2) + vplace * (D / 16);
-          if (W == 4) {
-            const uint2 u = *reinterpret_cast<const uint2*>(vp);
-            vw[x][0] = u.x, vw[x][W / 2 - 1] = u.y;
+          if constexpr (W == 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(vp);
+            vw[x][0] = v.x, vw[x][1] = v.y;
           } else {
             vw[x][0] = *reinterpret_cast<const uint32_t*>(vp);
           }
@@ -505,11 +568,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
           const uint32_t xx = __byte_perm(vw[0][h >> 1], vw[1][h >> 1], sel);
           const uint32_t yy = __byte_perm(vw[2][h >> 1], vw[3][h >> 1], sel);
           uint32_t c0[4], c1[4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            c0[n] = codes2<F32>(xx, n);
-            c1[n] = codes2<F32>(yy, n);
-          }
+          codes8(xx, c0);
+          codes8(yy, c1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -520,11 +580,31 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
             }
         }
       }
+    };
+
+    for (int t = t0; ok && t < t1; t += 2) {
+      const bool two = t + 1 < t1;
+      const int s0 = it % kStages, s1 = (it + 1) % kStages;
+      ok = wait_bounded(&full[s0], (it / kStages) & 1, guard);
+      if (ok && two) ok = wait_bounded(&full[s1], ((it + 1) / kStages) & 1, guard);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int tok0 = t * kTile + warp * 16, key0 = t * kTile + krow;
+      const uint8_t *st0 = smem + s0 * S::kStage, *st1 = smem + s1 * S::kStage;
+      if (two && tok0 + kTile + 16 <= lim_min)
+        keys32(std::false_type{}, st0, st1, key0, key0 + kTile);
+      else if (tok0 < len)
+        keys32(std::true_type{}, st0, two ? st1 : st0, key0, two ? key0 + kTile : INT_MAX - 16);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
+      if (lane == 0) {
+        mbar_arrive(&empty[s0]);
+        if (two) mbar_arrive(&empty[s1]);
+      }
+      it += two ? 2 : 1;
     }
 
     // ---- the CTA leaves the row: the warps' sums are joined
+    const float inv = 1.f / om;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -539,10 +619,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         }
 #pragma unroll
         for (int h = 0; h < W; ++h) {
-          const float add = fmaf(-BIAS, psum[nt][h * NG / W][x], off[nt][h * NG / W][x]);
+          const float add = off[nt][h * NG / W][x];
           *reinterpret_cast<float4*>(obuf + (warp * NQ + qi) * S::kORow + 32 * h + 4 * grp) =
-              make_float4(O[nt][2 * h][x] + add, O[nt][2 * h][2 + x] + add, O[nt][2 * h + 1][x] + add,
-                          O[nt][2 * h + 1][2 + x] + add);
+              make_float4(fmaf(O[nt][2 * h][x], inv, add), fmaf(O[nt][2 * h][2 + x], inv, add),
+                          fmaf(O[nt][2 * h + 1][x], inv, add), fmaf(O[nt][2 * h + 1][2 + x], inv, add));
         }
         if (grp == 0) ml[warp * NQ + qi] = make_float2(m2[nt][x], l[nt][x]);
       }
@@ -573,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
               make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         } else {
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * D + dim) =
-              make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+              make_uint2(pack2_bf16(o.x * inv, o.y * inv), pack2_bf16(o.z * inv, o.w * inv));
         }
         if (a.lse && dim == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
       } else {
@@ -641,7 +721,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const AttnArgs a, in
           make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     else
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + q * D + 4 * lane) =
-          make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+          make_uint2(pack2_bf16(o.x * inv, o.y * inv), pack2_bf16(o.z * inv, o.w * inv));
     if (a.lse && lane == 0) a.lse[q] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
   }
 }
