@@ -28,17 +28,18 @@
 // codes, free of bank conflicts by the page's order of words and the order in
 // which a tile's keys take the rows.
 //
-// Work. Rows are cut into tiles of 64 tokens; a row costs its tiles plus one.
+// Work. Rows are cut into tiles of 64 tokens; a row costs its tiles plus a
+// charge for starting and leaving it (an empty row 1).
 // The CTAs (up to three per SM) take equal shares of the total, contiguous
-// over rows; in a CTA one warp streams tiles into a ring of stages with bulk
-// copies (the four parts of a page's 64 tokens are each contiguous) and four
-// warps take 16 tokens of a tile each, with a softmax of their own that is
+// over rows; in a CTA one warp streams each row's queries and tiles into rings
+// of stages with bulk copies (the four parts of a page's 64 tokens are each
+// contiguous), running ahead over row ends, and four warps take 16 tokens of a
+// tile each, with a softmax of their own that is
 // joined when the CTA leaves the row. A row that several CTAs share leaves
 // partials, joined by paged_combine_kernel in CTA order. Every sum has a fixed
 // order.
 #include <cuda_fp16.h>
 
-#include <climits>
 #include <type_traits>
 
 #include "paged_common.cuh"
@@ -50,6 +51,7 @@ constexpr int kTile = 64;     // tokens per tile
 constexpr int kWarps = 4;     // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kStages = 5;
+constexpr int kRowCost = 2;   // of starting and leaving a row, in tiles
 constexpr float kGrow = 8.f;  // the running maximum moves when a logit passes it by this (log2 units)
 
 struct AttnArgs {
@@ -68,7 +70,7 @@ struct AttnArgs {
 };
 
 // Shared memory of a CTA.
-template <int D, int NG, int NT>
+template <int D, int NG, int NT, bool F32>
 struct Smem {
   static constexpr int kCode = kTile * D / 2, kScale = kTile * NG * 4;
   static constexpr int kV = kCode, kKs = 2 * kCode, kVs = kKs + kScale, kStage = kVs + kScale;
@@ -76,8 +78,10 @@ struct Smem {
   static constexpr int kObuf = kStages * kStage;
   static constexpr int kMl = kObuf + kWarps * NQ * kORow * 4;
   static constexpr int kBase = kMl + kWarps * NQ * 8;
-  static constexpr int kBar = (kBase + (kAttnRows + 1) * 4 + 15) / 16 * 16;
-  static constexpr int kBytes = kBar + 2 * kStages * 8 + 64;
+  static constexpr int kQ = (kBase + (kAttnRows + 1) * 4 + 15) / 16 * 16;  // two rows' queries
+  static constexpr int kQBytes = NQ * D * (F32 ? 4 : 2);
+  static constexpr int kBar = kQ + 2 * kQBytes;
+  static constexpr int kBytes = kBar + (2 * kStages + 4) * 8 + 48;
 };
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -145,9 +149,23 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // CTAs that share the work: at least two tiles' cost each.
 __device__ __forceinline__ int cta_count(int cost, int grid) { return max(1, min(grid, (cost + 1) / 2)); }
 
+__device__ __forceinline__ int row_cost(int len) { return len > 0 ? (len + kTile - 1) / kTile + kRowCost : 1; }
+
+// The tiles [t0, t1) of a row of cost [b0, b1) that the CTA with costs [lo, hi) takes.
+struct Share {
+  int tiles, t0, t1;
+};
+__device__ __forceinline__ Share share_of(int b0, int b1, int lo, int hi) {
+  Share s;
+  s.tiles = max(0, b1 - b0 - kRowCost);
+  s.t0 = max(lo - b0 - kRowCost, 0);
+  s.t1 = min(s.tiles, hi - b0 - kRowCost);
+  return s;
+}
+
 template <int D, int NG, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2) paged_attn_kernel(const AttnArgs a) {
-  using S = Smem<D, NG, NT>;
+  using S = Smem<D, NG, NT, F32>;
   constexpr int W = D / 32, NQ = S::NQ, PARTS = F32 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   float* obuf = reinterpret_cast<float*>(smem + S::kObuf);
@@ -155,8 +173,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
   int* base = reinterpret_cast<int*>(smem + S::kBase);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBar);
   uint64_t* empty = full + kStages;
-  int* wsum = reinterpret_cast<int*>(empty + kStages);
-  volatile int* abort_flag = wsum + 8;
+  uint64_t* q_full = empty + kStages;  // [2], by the parity of the row's number in this CTA
+  uint64_t* q_empty = q_full + 2;
+  int* wsum = reinterpret_cast<int*>(q_empty + 2);
+  int* q_len = wsum + 8;  // [2]
+  volatile int* abort_flag = wsum + 10;
   const PageGeom& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -164,6 +185,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], kWarps);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -183,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         if (blockIdx.x == 0) atomicOr(a.c.status, KV_DEV_BOUNDS);
       }
       base[i] = sum;  // made absolute below
-      sum += (n + kTile - 1) / kTile + 1;
+      sum += row_cost(n);
     }
     int incl = sum;
 #pragma unroll
@@ -219,10 +244,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     row = x;
   }
   if (threadIdx.x == 0 && chunk == 0) {
-    const int t0 = lo - base[row] - 1;  // > 0: the row's first tiles are another CTA's
+    const int t0 = lo - base[row] - kRowCost;  // > 0: the row's first tiles are another CTA's
     int4 rec = make_int4(-1, 0, 0, 0);
     if (t0 > 0) {
-      const int f = (int)(((long long)(base[row] + 2) * n_cta - 1) / cost);  // holds the row's first tile
+      const int f = (int)(((long long)(base[row] + kRowCost + 1) * n_cta - 1) / cost);  // holds the row's first tile
       const int l = (int)(((long long)base[row + 1] * n_cta - 1) / cost);    // holds its last
       if (f + 1 == cta) rec = make_int4(row, f, l, 0);
     }
@@ -239,15 +264,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     const int sec_page = sec == 0 ? 0 : sec == 1 ? g.v : sec == 2 ? g.ks : g.vs;
     const int sec_stage = sec == 0 ? 0 : sec == 1 ? S::kV : sec == 2 ? S::kKs : S::kVs;
     const uint32_t tok_bytes = sec < 2 ? D / 2 : NG * 4;
-    int it = 0;
+    const int q0 = chunk * NQ, nq = min(NQ, a.R - q0);
+    constexpr int EB = F32 ? 4 : 2;
+    int it = 0, k = 0;
     bool ok = true;
     for (int r = row; ok && r < a.n_rows && base[r] < hi; ++r) {
-      const int tiles = base[r + 1] - base[r] - 1;
-      const int t0 = max(lo - base[r] - 1, 0), t1 = min(tiles, hi - base[r] - 1);
+      const auto [tiles, t0, t1] = share_of(base[r], base[r + 1], lo, hi);
       if (t0 >= t1) continue;
       const int trow = table_row(a.rows, a.row0 + r);
       const int32_t* list = a.c.table + (size_t)trow * g.max_pages;
-      const int np = (a.c.len[trow] + g.P - 1) >> g.log_p;
+      const int len = a.c.len[trow];
+      const int np = (len + g.P - 1) >> g.log_p;
+      if (k >= 2) ok = wait_bounded(&q_empty[k & 1], ((k >> 1) - 1) & 1, guard);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        const uint32_t bytes = (uint32_t)(nq * D * EB);
+        q_len[k & 1] = len;
+        mbar_arrive_expect_tx(&q_full[k & 1], bytes);
+        bulk_load(smem + S::kQ + (k & 1) * S::kQBytes,
+                  static_cast<const uint8_t*>(a.q) + ((long long)(a.row0 + r) * a.R + q0) * (D * EB), bytes,
+                  &q_full[k & 1]);
+      }
+      ++k;
       int win = -32, entry = 0;  // lane l holds page number list[win + l]
       for (int t = t0; t < t1; ++t, ++it) {
         const int j0 = (t * kTile) >> g.log_p;
@@ -274,7 +313,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       }
     }
     // copies in flight land before the CTA gives its memory back, also when the others have given up
-    for (int k = max(0, it - kStages); k < it; ++k) wait_drain(&full[k % kStages], (k / kStages) & 1);
+    for (int i = max(0, it - kStages); i < it; ++i) wait_drain(&full[i % kStages], (i / kStages) & 1);
+    for (int i = max(0, k - 2); i < k; ++i) wait_drain(&q_full[i & 1], (i >> 1) & 1);
     return;
   }
 
@@ -285,15 +325,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
   const int krow = warp * 16 + ((grp & 1) ? 4 + ((grp >> 1) ^ 1) : grp >> 1);
   const int vrow = warp * 16 + tig, vrow2 = warp * 16 + 4 + (tig ^ 1);
   const int vplace = grp ^ ((tig & 2) << 1);
-  int it = 0;
+  const int q0 = chunk * NQ, nq = min(NQ, a.R - q0);
+  int it = 0, k = 0;
   bool ok = true;
   for (int r = row; r < a.n_rows && base[r] < hi; ++r) {
-    const int tiles = base[r + 1] - base[r] - 1;
-    const int t0 = max(lo - base[r] - 1, 0), t1 = min(tiles, hi - base[r] - 1);
+    const auto [tiles, t0, t1] = share_of(base[r], base[r + 1], lo, hi);
     const int crow = a.row0 + r;
-    if (tiles > 0 && t0 >= t1) continue;
-    const int q0 = chunk * NQ, nq = min(NQ, a.R - q0);
-    const int len = tiles > 0 ? a.c.len[table_row(a.rows, crow)] : 0;
+    if (t0 >= t1) {
+      if (tiles == 0) {  // an empty row
+        const long long at = (long long)crow * a.R + q0;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + at * (D * (F32 ? 4 : 2)));
+        for (int i = threadIdx.x; i < nq * D * (F32 ? 4 : 2) / 16; i += kWarps * 32) o[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse && (int)threadIdx.x < nq) a.lse[at + threadIdx.x] = -INFINITY;
+      }
+      continue;
+    }
+    ok = wait_bounded(&q_full[k & 1], (k >> 1) & 1, guard);
+    ok = __all_sync(0xffffffffu, ok);
+    const int len = q_len[k & 1];
+    const uint8_t* qs = smem + S::kQ + (k & 1) * S::kQBytes;
 
     // query fragments, their sums by group, and what turns a sum into a logit in log2 units
     uint32_t qf[NT][PARTS][W][4];
@@ -304,15 +354,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       float x[W][8], top = 0.f, sum[NG];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const long long at = ((long long)crow * a.R + q0 + qi) * D + 32 * w + 8 * tig;
+        const int at = qi * D + 32 * w + 8 * tig;
         if (qi < nq) {
           if (F32) {
-            const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
-            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 4);
+            const float4 u = *reinterpret_cast<const float4*>(qs + at * 4);
+            const float4 v = *reinterpret_cast<const float4*>(qs + at * 4 + 16);
             x[w][0] = u.x, x[w][1] = u.y, x[w][2] = u.z, x[w][3] = u.w;
             x[w][4] = v.x, x[w][5] = v.y, x[w][6] = v.z, x[w][7] = v.w;
           } else {
-            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+            const uint4 u = *reinterpret_cast<const uint4*>(qs + at * 2);
             x[w][0] = lo_f(u.x), x[w][1] = hi_f(u.x), x[w][2] = lo_f(u.y), x[w][3] = hi_f(u.y);
             x[w][4] = lo_f(u.z), x[w][5] = hi_f(u.z), x[w][6] = lo_f(u.w), x[w][7] = hi_f(u.w);
           }
@@ -357,6 +407,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         unit[nt][c] = __shfl_sync(0xffffffffu, down, (2 * tig + c) * 4);
       }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_empty[k & 1]);
+    ++k;
     // keys that this lane's queries see
     int lim[NT][2];
     const int lim_min = len - a.n_q + 1;
@@ -382,12 +435,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     }
     float om = 1.f, s_top = -1.f;  // scale of p', and the largest step that it is made for
 
-    // 16 keys from each of two stages; MASKED: some are hidden from some query, or (key >= none) not there.
-    auto keys32 = [&](auto mk, const uint8_t* st0, const uint8_t* st1, int key0, int key1) {
-      constexpr bool MASKED = decltype(mk)::value;
-      constexpr int U = 2;
-      const uint8_t* sts[U] = {st0, st1};
-      const int keys[U] = {key0, key1};  // of matrix row grp; row grp + 8 is 8 further
+    // 16 keys from each of U stages, of tiles t and after; MASKED (U = 1): some are hidden from some query.
+    auto attend = [&](auto uu, const uint8_t* st0, const uint8_t* st1, int t) {
+      constexpr int U = decltype(uu)::value;
+      constexpr bool MASKED = U == 1;
+      const uint8_t* sts[2] = {st0, st1};
+      const int key0 = t * kTile + krow;  // of matrix row grp; row grp + 8 is 8 further
       // ---- logits: rows keys, columns queries
       float y[U][NT][4];
 #pragma unroll
@@ -444,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              if (keys[u] + 8 * (x >> 1) >= lim[nt][x & 1]) y[u][nt][x] = -INFINITY;
+              if (key0 + 8 * (x >> 1) >= lim[nt][x & 1]) y[u][nt][x] = -INFINITY;
         }
       }
       uint32_t vs[U][2][NG];
@@ -454,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         for (int x = 0; x < 2; ++x) {
           load_scales<NG>(sts[u] + S::kVs + (krow + 8 * x) * (NG * 4), vs[u][x]);
           if constexpr (MASKED) {
-            if (keys[u] + 8 * x >= len) {
+            if (key0 + 8 * x >= len) {
 #pragma unroll
               for (int z = 0; z < NG; ++z) vs[u][x][z] = 0;  // what lies there may be NaN
             }
@@ -492,7 +545,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float mx = fmaxf(fmaxf(y[0][nt][x], y[0][nt][2 + x]), fmaxf(y[1][nt][x], y[1][nt][2 + x]));
+            float mx = fmaxf(y[0][nt][x], y[0][nt][2 + x]);
+            if constexpr (U == 2) mx = fmaxf(mx, fmaxf(y[1][nt][x], y[1][nt][2 + x]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const float now = fmaxf(m2[nt][x], mx * unit[nt][x]);
@@ -519,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
           bool seen[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            seen[x] = !MASKED || keys[u] + 8 * (x >> 1) < lim[nt][x & 1];
+            seen[x] = !MASKED || key0 + 8 * (x >> 1) < lim[nt][x & 1];
             p[x] = ex2_approx(fmaf(y[u][nt][x], unit[nt][x & 1], -m2[nt][x & 1]));
             if (!seen[x]) p[x] = 0.f;
             l[nt][x & 1] += p[x];
@@ -582,25 +636,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       }
     };
 
-    for (int t = t0; ok && t < t1; t += 2) {
-      const bool two = t + 1 < t1;
+    for (int t = t0; ok && t < t1;) {
+      // two tiles at once while every query sees all of them
+      const int n = t + 2 <= t1 && (t + 1) * kTile + warp * 16 + 16 <= lim_min ? 2 : 1;
       const int s0 = it % kStages, s1 = (it + 1) % kStages;
       ok = wait_bounded(&full[s0], (it / kStages) & 1, guard);
-      if (ok && two) ok = wait_bounded(&full[s1], ((it + 1) / kStages) & 1, guard);
+      if (ok && n == 2) ok = wait_bounded(&full[s1], ((it + 1) / kStages) & 1, guard);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const int tok0 = t * kTile + warp * 16, key0 = t * kTile + krow;
       const uint8_t *st0 = smem + s0 * S::kStage, *st1 = smem + s1 * S::kStage;
-      if (two && tok0 + kTile + 16 <= lim_min)
-        keys32(std::false_type{}, st0, st1, key0, key0 + kTile);
-      else if (tok0 < len)
-        keys32(std::true_type{}, st0, two ? st1 : st0, key0, two ? key0 + kTile : INT_MAX - 16);
+      if (n == 2)
+        attend(std::integral_constant<int, 2>{}, st0, st1, t);
+      else if (t * kTile + warp * 16 < len)
+        attend(std::integral_constant<int, 1>{}, st0, st1, t);
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&empty[s0]);
-        if (two) mbar_arrive(&empty[s1]);
+        if (n == 2) mbar_arrive(&empty[s1]);
       }
-      it += two ? 2 : 1;
+      t += n;
+      it += n;
     }
 
     // ---- the CTA leaves the row: the warps' sums are joined
@@ -743,7 +798,7 @@ int launch_pdl(K k, dim3 grid, int threads, size_t smem, cudaStream_t st, A... a
 
 template <int D, int NG, int NT, bool F32>
 int run(AttnArgs a, cudaStream_t st) {
-  using S = Smem<D, NG, NT>;
+  using S = Smem<D, NG, NT, F32>;
   auto k = paged_attn_kernel<D, NG, NT, F32>;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
     return KV_ERR_CUDA;
