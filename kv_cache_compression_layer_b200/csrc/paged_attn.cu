@@ -54,21 +54,6 @@ constexpr int kStages = 5;
 constexpr int kRowCost = 2;   // of starting and leaving a row, in tiles
 constexpr float kGrow = 8.f;  // the running maximum moves when a logit passes it by this (log2 units)
 
-struct AttnArgs {
-  PageGeom g;
-  SeqRows rows;
-  PagedCache c;
-  int row0, n_rows;  // call rows of this launch
-  int n_q, group, R; // R = n_q * group
-  float scale2;      // log2(e) / sqrt(d)
-  const void* q;
-  void* out;
-  float* lse;
-  int4* split;       // [CTAs]: a row whose second CTA this is (row, first CTA, last CTA), or -1
-  float* part;
-  unsigned long long limit_ns;
-};
-
 // Shared memory of a CTA.
 template <int D, int NG, int NT, bool F32>
 struct Smem {
@@ -117,14 +102,41 @@ __device__ __forceinline__ uint32_t add2(uint32_t x, uint32_t y) {
   return r;
 }
 
-// The four nibble pairs of x (bits 4 n and 16 + 4 n) as two fp16 each: c - 8.
-__device__ __forceinline__ void codes8(uint32_t x, uint32_t (&c)[4]) {
-  const uint32_t y = x >> 8;
-  c[0] = add2((x & 0x000f000fu) | 0x64006400u, 0xe408e408u);
-  c[1] = add2((x & 0x00f000f0u) | 0x54005400u, 0xd480d480u);
-  c[2] = add2((y & 0x000f000fu) | 0x64006400u, 0xe408e408u);
-  c[3] = add2((y & 0x00f000f0u) | 0x54005400u, 0xd480d480u);
+// (x & mask) | bits in one instruction: it takes one constant, so the other comes in a register.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "n"(MASK), "r"(bits));
+  return r;
 }
+// The four nibble pairs of x (bits 4 n and 16 + 4 n) as two fp16 each: c - 8.
+struct CodeConst {
+  uint32_t k10, k6;  // 1024 and 64 in both halves: the bits that make a number of a code
+  uint32_t s10, s6;  // -1032 and -72: what makes it c - 8
+};
+__device__ __forceinline__ void codes8(uint32_t x, const CodeConst& k, uint32_t (&c)[4]) {
+  const uint32_t y = x >> 8;
+  c[0] = add2(pick<0x000f000fu>(x, k.k10), k.s10);
+  c[1] = add2(pick<0x00f000f0u>(x, k.k6), k.s6);
+  c[2] = add2(pick<0x000f000fu>(y, k.k10), k.s10);
+  c[3] = add2(pick<0x00f000f0u>(y, k.k6), k.s6);
+}
+struct AttnArgs {
+  PageGeom g;
+  SeqRows rows;
+  PagedCache c;
+  int row0, n_rows;  // call rows of this launch
+  int n_q, group, R; // R = n_q * group
+  float scale2;      // log2(e) / sqrt(d)
+  const void* q;
+  void* out;
+  float* lse;
+  int4* split;       // [CTAs]: a row whose second CTA this is (row, first CTA, last CTA), or -1
+  float* part;
+  unsigned long long limit_ns;
+  CodeConst kc;  // an argument, so that the constants stay in registers
+};
+
 // The NG scales of a token.
 template <int NG>
 __device__ __forceinline__ void load_scales(const uint8_t* p, uint32_t (&s)[NG]) {
@@ -320,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
 
   // -------------------------------------------------------------- consumers
   const int grp = lane >> 2, tig = lane & 3;
+  const CodeConst kc = a.kc;
   // Matrix row r of a half tile is token tok(r): rows 2 t and 2 t + 1 are tokens t and 4 + (t ^ 1), so that the
   // lanes of a K load and of a V load fall on different banks.
   const int krow = warp * 16 + ((grp & 1) ? 4 + ((grp >> 1) ^ 1) : grp >> 1);
@@ -469,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           uint32_t c0[4], c1[4];
-          codes8(kw[0][w], c0);
-          codes8(kw[1][w], c1);
+          codes8(kw[0][w], kc, c0);
+          codes8(kw[1][w], kc, c1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -622,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
           const uint32_t xx = __byte_perm(vw[0][h >> 1], vw[1][h >> 1], sel);
           const uint32_t yy = __byte_perm(vw[2][h >> 1], vw[3][h >> 1], sel);
           uint32_t c0[4], c1[4];
-          codes8(xx, c0);
-          codes8(yy, c1);
+          codes8(xx, kc, c0);
+          codes8(yy, kc, c1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -842,6 +855,7 @@ int launch_paged_attn(const kv_paged_shape& sh, const PageGeom& g, const SeqRows
   a.split = reinterpret_cast<int4*>(ws + w.att_base);
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.limit_ns = wait_limit_ns();
+  a.kc = {0x64006400u, 0x54005400u, 0xe408e408u, 0xd480d480u};
   const bool f32 = sh.dtype == KV_F32;
   if (g.d == 64) return g.G == 1 ? run_as<64, 1>(a, f32, st) : run_as<64, 2>(a, f32, st);
   return g.G == 1 ? run_as<128, 1>(a, f32, st) : g.G == 2 ? run_as<128, 2>(a, f32, st) : run_as<128, 4>(a, f32, st);
