@@ -283,12 +283,112 @@ __device__ __noinline__ uint32_t code_exact(float x, float m, float s) {
   const double q = ((double)x - (double)m) / (double)s;
   return (uint32_t)rint(fmin(fmax(q, 0.0), 15.0));
 }
+// float32 of (mx - m) / 15, taken in float64.
+__device__ __noinline__ float step_exact(float mx, float m) { return (float)(((double)mx - (double)m) / 15.0); }
+
+// Two float32 in one register pair, and the packed operations on them.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Codes of the 8 channels that a lane holds of a group with largest value mx
+// and base m (bf16 of the smallest): channel n in bits 4 n; *scale the packed
+// (s, m). All of it is exact arithmetic's result. The step: the float32 product
+// is off by a few of its last bits, so where it lies next to the middle of two
+// bf16 the quotient is taken in float64. The codes: x - m is exact in float32
+// unless the two lie far apart, and q = RN((x - m) / s) follows from the
+// rounded reciprocal by one correction with the exact remainder; it is a half
+// only if the exact quotient is (one that is not differs from a half by the
+// last bit of x - m over s at least, more than half the last bit of q). Where
+// x - m was rounded (bf16: rare; F32: mostly, then only a quotient within 1e-5
+// of a half matters) the codes are taken in float64.
+template <bool F32>
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float mx, float m, uint32_t* scale) {
+  if (!(fabsf(mx) < INFINITY && fabsf(m) < INFINITY)) {
+    *scale = 0x7fff7fffu;  // (NaN, NaN)
+    return 0u;
+  }
+  float s = 0.f;
+  if (mx > m) {
+    float f = __fmul_rn(__fsub_rn(mx, m), 1.f / 15.f);
+    const uint32_t low = __float_as_uint(f) & 0xffffu;
+    if (low - 0x7fe0u <= 0x40u || !(f > 1e-30f) || !(f < 1e37f)) f = step_exact(mx, m);
+    s = bf16_round(f);
+  }
+  *scale = bf16_bits(s) | (__float_as_uint(m) & 0xffff0000u);
+  if (s == 0.f) return 0u;
+  uint32_t w = 0;
+  bool exact = false;
+  if (s > 1e-30f) {
+    const float magic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits of the sum
+    const float r = __frcp_rn(s);
+    const uint64_t m2 = f2(m, m), nm2 = f2(-m, -m), r2 = f2(r, r), ns2 = f2(-s, -s), g2 = f2(magic, magic),
+                   n1 = f2(-1.f, -1.f);
+    uint32_t off = 0;
+    float dev = 0.f;
+#pragma unroll
+    for (int n = 6; n >= 0; n -= 2) {
+      const uint64_t v = f2(x[n], x[n + 1]);
+      const uint64_t t = add2(v, nm2);
+      const uint64_t q0 = mul2(t, r2);
+      uint64_t q = fma2(fma2(q0, ns2, t), r2, q0);
+      if (F32) {  // the base may be above the smallest
+        float a, b;
+        unpack2(q, a, b);
+        q = f2(fmaxf(a, 0.f), fmaxf(b, 0.f));
+      }
+      const uint64_t y = add2(q, g2);
+      float y0, y1, e0, e1;
+      unpack2(y, y0, y1);
+      if (F32) {
+        float a, b;
+        unpack2(fma2(add2(y, f2(-magic, -magic)), n1, q), a, b);
+        dev = fmaxf(dev, fmaxf(fabsf(a), fabsf(b)));
+      }
+      unpack2(fma2(v, n1, add2(t, m2)), e0, e1);  // 0 where t is exact
+      off |= __float_as_uint(e0) | __float_as_uint(e1);
+      w = (w << 4) + __float_as_uint(y1);
+      w = (w << 4) + __float_as_uint(y0);
+    }
+    w -= 0x3F400000u;  // what the eight shifted exponents of `magic` (0x4B400000) add up to
+    exact = (off & 0x7fffffffu) == 0u || (F32 && dev <= 0.49999f);
+  }
+  if (!exact) {
+    w = 0;
+#pragma unroll
+    for (int n = 7; n >= 0; --n) w = (w << 4) | code_exact(x[n], m, s);
+  }
+  return w;
+}
+
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 // Quantises the 8 channels that a lane holds of a group spread over LG
-// consecutive lanes: the codes, channel n in bits 4 n; *scale the packed (s, m).
-// The float32 products are off by a few of their last bits, so where that
-// could tip a rounding (a step next to the middle of two bf16, a quotient
-// within 1e-5 of a half) the decision is made again in float64.
+// consecutive lanes. NaN and infinities reach mx or m.
 template <int LG>
 __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t* scale) {
   float mx = x[0], mn = x[0];
@@ -302,41 +402,18 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t* sca
     mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
   }
-  const float m = bf16_round(mn);
-  if (!(fabsf(mx) < INFINITY && fabsf(mn) < INFINITY && fabsf(m) < INFINITY)) {
-    *scale = 0x7fff7fffu;  // (NaN, NaN)
-    return 0u;
-  }
-  float s = 0.f;
-  if (mx > m) {
-    float f = __fmul_rn(__fsub_rn(mx, m), 1.f / 15.f);
-    const uint32_t low = __float_as_uint(f) & 0xffffu;
-    if (low - 0x7fe0u <= 0x40u || !(f > 1e-30f) || !(f < 1e37f)) f = (float)(((double)mx - (double)m) / 15.0);
-    s = bf16_round(f);
-  }
-  *scale = bf16_bits(s) | (bf16_bits(m) << 16);
-  if (s == 0.f) return 0u;
-  uint32_t w = 0;
-  float dev = 1.f;
-  if (s > 1e-30f) {
-    const float magic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits of the sum
-    const float r = __frcp_rn(s);
-    dev = 0.f;
+  return codes_of<true>(x, mx, bf16_round(mn), scale);
+}
+// The same of bf16 channels: the largest and the negated smallest share a register.
+template <int LG>
+__device__ __forceinline__ uint32_t quantise8(const uint4& u, const float (&x)[8], uint32_t* scale) {
+  const uint32_t neg = 0x80008000u;
+  const uint32_t hi = max2_nan(max2_nan(u.x, u.y), max2_nan(u.z, u.w));
+  const uint32_t lo = max2_nan(max2_nan(u.x ^ neg, u.y ^ neg), max2_nan(u.z ^ neg, u.w ^ neg));
+  uint32_t v = max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
 #pragma unroll
-    for (int n = 7; n >= 0; --n) {
-      const float q = fmaxf(__fmul_rn(__fsub_rn(x[n], m), r), 0.f);
-      const float y = __fadd_rn(q, magic);
-      dev = fmaxf(dev, fabsf(__fsub_rn(q, __fsub_rn(y, magic))));
-      w = (w << 4) + __float_as_uint(y);
-    }
-    w -= 0x3F400000u;  // what the eight shifted exponents of `magic` (0x4B400000) add up to
-  }
-  if (dev > 0.49999f) {
-    w = 0;
-#pragma unroll
-    for (int n = 7; n >= 0; --n) w = (w << 4) | code_exact(x[n], m, s);
-  }
-  return w;
+  for (int o = 1; o < LG; o <<= 1) v = max2_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return codes_of<false>(x, __uint_as_float(v << 16), __uint_as_float((v & 0xffff0000u) ^ 0x80000000u), scale);
 }
 
 // The same 8 channels back: m + c s, one rounding in float32.
@@ -367,6 +444,10 @@ struct Row8<false> {
       x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
     }
   }
+  template <int LG>
+  __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t* scale) const {
+    return quantise8<LG>(u, x, scale);
+  }
   static __device__ __forceinline__ void store(void* base, long long row, int d, int l, const float (&x)[8]) {
     uint32_t v[4];
 #pragma unroll
@@ -389,6 +470,10 @@ struct Row8<true> {
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
     x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  template <int LG>
+  __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t* scale) const {
+    return quantise8<LG>(x, scale);
   }
   static __device__ __forceinline__ void store(void* base, long long row, int d, int l, const float (&x)[8]) {
     float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + row * d) + 2 * l;
@@ -485,11 +570,11 @@ __global__ void __launch_bounds__(kMoveWarps * 32) paged_store_kernel(const Stor
       float x[8];
       uint32_t sc;
       k[it].get(x);
-      uint32_t code = quantise8<QG / 8>(x, &sc);
+      uint32_t code = k[it].template quantise<QG / 8>(x, &sc);
       reinterpret_cast<uint32_t*>(st)[t * (D / 8) + (l & 3) * W + (l >> 2)] = code;
       if (l % (QG / 8) == 0) reinterpret_cast<uint32_t*>(st + 2 * kCode)[t * G + l / (QG / 8)] = sc;
       v[it].get(x);
-      code = quantise8<QG / 8>(x, &sc);
+      code = v[it].template quantise<QG / 8>(x, &sc);
       const int pv = (2 * (l & 3)) ^ ((t & 2) << 1);  // place of channels 8 l .. 8 l + 3; the next four follow
       uint16_t* sv = reinterpret_cast<uint16_t*>(st + kCode) + t * (D / 4) + pv * W + (l >> 2);
       sv[0] = (uint16_t)code;
