@@ -279,9 +279,16 @@ __device__ __forceinline__ uint32_t bf16_bits(float x) { return __bfloat16_as_us
 
 // The code of x by its definition, in float64: the quotient's rounding does
 // not reach a half (x, m and s have at most 24, 8 and 8 bits).
-__device__ __noinline__ uint32_t code_exact(float x, float m, float s) {
+__device__ __forceinline__ uint32_t code_exact(float x, float m, float s) {
   const double q = ((double)x - (double)m) / (double)s;
   return (uint32_t)rint(fmin(fmax(q, 0.0), 15.0));
+}
+// Eight of them (a call: the common path keeps its registers and its place in the instruction cache).
+__device__ __noinline__ uint32_t codes_exact(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
+                                             float x7, float m, float s) {
+  uint32_t w = code_exact(x0, m, s) | code_exact(x1, m, s) << 4 | code_exact(x2, m, s) << 8;
+  w |= code_exact(x3, m, s) << 12 | code_exact(x4, m, s) << 16 | code_exact(x5, m, s) << 20;
+  return w | code_exact(x6, m, s) << 24 | code_exact(x7, m, s) << 28;
 }
 // float32 of (mx - m) / 15, taken in float64.
 __device__ __noinline__ float step_exact(float mx, float m) { return (float)(((double)mx - (double)m) / 15.0); }
@@ -311,22 +318,23 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// Codes of the 8 channels that a lane holds of a group with largest value mx
-// and base m (bf16 of the smallest): channel n in bits 4 n; *scale the packed
-// (s, m). All of it is exact arithmetic's result. The step: the float32 product
-// is off by a few of its last bits, so where it lies next to the middle of two
-// bf16 the quotient is taken in float64. The codes: x - m is exact in float32
-// unless the two lie far apart, and q = RN((x - m) / s) follows from the
-// rounded reciprocal by one correction with the exact remainder; it is a half
-// only if the exact quotient is (one that is not differs from a half by the
-// last bit of x - m over s at least, more than half the last bit of q). Where
-// x - m was rounded (bf16: rare; F32: mostly, then only a quotient within 1e-5
-// of a half matters) the codes are taken in float64.
+// Codes of the 16 channels that a lane holds of a group with largest value mx
+// and base m (bf16 of the smallest): channels 8 i + n in bits 4 n of w[i];
+// *scale the packed (s, m). All of it is exact arithmetic's result. The step:
+// the float32 product is off by a few of its last bits, so where it lies next
+// to the middle of two bf16 the quotient is taken in float64. The codes: x - m
+// is exact in float32 unless the two lie far apart, and q = RN((x - m) / s)
+// follows from the rounded reciprocal by one correction with the exact
+// remainder; it is a half only if the exact quotient is (one that is not
+// differs from a half by the last bit of x - m over s at least, more than half
+// the last bit of q). Where x - m was rounded (bf16: rare; F32: mostly, then
+// only a quotient within 1e-5 of a half matters) the codes are taken in float64.
 template <bool F32>
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float mx, float m, uint32_t* scale) {
+__device__ __forceinline__ void codes_of(const float (&x)[16], float mx, float m, uint32_t (&w)[2], uint32_t* scale) {
+  w[0] = w[1] = 0u;
   if (!(fabsf(mx) < INFINITY && fabsf(m) < INFINITY)) {
     *scale = 0x7fff7fffu;  // (NaN, NaN)
-    return 0u;
+    return;
   }
   float s = 0.f;
   if (mx > m) {
@@ -336,8 +344,7 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float mx, floa
     s = bf16_round(f);
   }
   *scale = bf16_bits(s) | (__float_as_uint(m) & 0xffff0000u);
-  if (s == 0.f) return 0u;
-  uint32_t w = 0;
+  if (s == 0.f) return;
   bool exact = false;
   if (s > 1e-30f) {
     const float magic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits of the sum
@@ -347,7 +354,7 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float mx, floa
     uint32_t off = 0;
     float dev = 0.f;
 #pragma unroll
-    for (int n = 6; n >= 0; n -= 2) {
+    for (int n = 14; n >= 0; n -= 2) {
       const uint64_t v = f2(x[n], x[n + 1]);
       const uint64_t t = add2(v, nm2);
       const uint64_t q0 = mul2(t, r2);
@@ -367,18 +374,17 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float mx, floa
       }
       unpack2(fma2(v, n1, add2(t, m2)), e0, e1);  // 0 where t is exact
       off |= __float_as_uint(e0) | __float_as_uint(e1);
-      w = (w << 4) + __float_as_uint(y1);
-      w = (w << 4) + __float_as_uint(y0);
+      w[n >> 3] = (w[n >> 3] << 4) + __float_as_uint(y1);
+      w[n >> 3] = (w[n >> 3] << 4) + __float_as_uint(y0);
     }
-    w -= 0x3F400000u;  // what the eight shifted exponents of `magic` (0x4B400000) add up to
+    w[0] -= 0x3F400000u;  // what the eight shifted exponents of `magic` (0x4B400000) add up to
+    w[1] -= 0x3F400000u;
     exact = (off & 0x7fffffffu) == 0u || (F32 && dev <= 0.49999f);
   }
   if (!exact) {
-    w = 0;
-#pragma unroll
-    for (int n = 7; n >= 0; --n) w = (w << 4) | code_exact(x[n], m, s);
+    w[0] = codes_exact(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], m, s);
+    w[1] = codes_exact(x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15], m, s);
   }
-  return w;
 }
 
 __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
@@ -387,100 +393,110 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Quantises the 8 channels that a lane holds of a group spread over LG
-// consecutive lanes. NaN and infinities reach mx or m.
-template <int LG>
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t* scale) {
-  float mx = x[0], mn = x[0];
-#pragma unroll
-  for (int n = 1; n < 8; ++n) {
-    mx = max_nan(mx, x[n]);
-    mn = min_nan(mn, x[n]);
-  }
-#pragma unroll
-  for (int o = 1; o < LG; o <<= 1) {
-    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-  }
-  return codes_of<true>(x, mx, bf16_round(mn), scale);
-}
-// The same of bf16 channels: the largest and the negated smallest share a register.
-template <int LG>
-__device__ __forceinline__ uint32_t quantise8(const uint4& u, const float (&x)[8], uint32_t* scale) {
-  const uint32_t neg = 0x80008000u;
-  const uint32_t hi = max2_nan(max2_nan(u.x, u.y), max2_nan(u.z, u.w));
-  const uint32_t lo = max2_nan(max2_nan(u.x ^ neg, u.y ^ neg), max2_nan(u.z ^ neg, u.w ^ neg));
-  uint32_t v = max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
-#pragma unroll
-  for (int o = 1; o < LG; o <<= 1) v = max2_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return codes_of<false>(x, __uint_as_float(v << 16), __uint_as_float((v & 0xffff0000u) ^ 0x80000000u), scale);
-}
-
-// The same 8 channels back: m + c s, one rounding in float32.
-__device__ __forceinline__ void dequantise8(uint32_t w, uint32_t scale, float (&x)[8]) {
-  const float s = __uint_as_float(scale << 16), m = __uint_as_float(scale & 0xffff0000u);
-#pragma unroll
-  for (int n = 0; n < 8; ++n) {
-    const float c = __uint_as_float(0x4B000000u | ((w >> (4 * n)) & 15u)) - 8388608.f;  // exact
-    x[n] = fmaf(c, s, m);
-  }
-}
-
-// 8 channels of a row, 16-byte loads and stores.
+// 16 channels of a row: loaded with 16-byte loads, quantised with the LG
+// consecutive lanes that hold the rest of their group (NaN and infinities
+// reach the group's largest or smallest).
 template <bool F32>
-struct Row8;
+struct Row16;
 template <>
-struct Row8<false> {
-  uint4 u;
+struct Row16<false> {
+  uint4 a, b;
   __device__ __forceinline__ void load(const void* base, long long row, int d, int l) {
-    u = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + row * d)[l];
-  }
-  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(v[i] << 16);
-      x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-    }
-  }
-  template <int LG>
-  __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t* scale) const {
-    return quantise8<LG>(u, x, scale);
-  }
-  static __device__ __forceinline__ void store(void* base, long long row, int d, int l, const float (&x)[8]) {
-    uint32_t v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      v[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + row * d)[l] = make_uint4(v[0], v[1], v[2], v[3]);
-  }
-};
-template <>
-struct Row8<true> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* base, long long row, int d, int l) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + row * d) + 2 * l;
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + row * d) + 2 * l;
     a = p[0];
     b = p[1];
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  template <int LG>
+  __device__ __forceinline__ void quantise(uint32_t (&w)[2], uint32_t* scale) const {
+    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const uint32_t neg = 0x80008000u;
+    uint32_t hi = u[0], lo = u[0] ^ neg;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi = max2_nan(hi, u[i]);
+      lo = max2_nan(lo, u[i] ^ neg);
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+    // the largest and the negated smallest share a register
+    uint32_t v = max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
+#pragma unroll
+    for (int o = 1; o < LG; o <<= 1) v = max2_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    codes_of<false>(x, __uint_as_float(v << 16), __uint_as_float((v & 0xffff0000u) ^ 0x80000000u), w, scale);
+  }
+};
+template <>
+struct Row16<true> {
+  float4 v[4];
+  __device__ __forceinline__ void load(const void* base, long long row, int d, int l) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + row * d) + 4 * l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = p[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   template <int LG>
-  __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t* scale) const {
-    return quantise8<LG>(x, scale);
+  __device__ __forceinline__ void quantise(uint32_t (&w)[2], uint32_t* scale) const {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[4 * i] = v[i].x, x[4 * i + 1] = v[i].y, x[4 * i + 2] = v[i].z, x[4 * i + 3] = v[i].w;
+    float mx = x[0], mn = x[0];
+#pragma unroll
+    for (int n = 1; n < 16; ++n) {
+      mx = max_nan(mx, x[n]);
+      mn = min_nan(mn, x[n]);
+    }
+#pragma unroll
+    for (int o = 1; o < LG; o <<= 1) {
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    }
+    codes_of<true>(x, mx, bf16_round(mn), w, scale);
   }
-  static __device__ __forceinline__ void store(void* base, long long row, int d, int l, const float (&x)[8]) {
+};
+
+// (x & mask) | bits in one instruction: it takes one constant, so the other comes in a register.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "n"(MASK), "r"(bits));
+  return r;
+}
+
+// Writes the 8 channels of codes w as m + c s, rounded once, with 16-byte
+// stores. bf16: bits 0-3 of a half or-ed into 0x4300 are 128 + c, so two
+// channels take a subtraction and a multiply-add in bf16. float32: the code
+// or-ed into 2^23. `bits` is 0x43004300 or 0x4B000000.
+template <bool F32>
+__device__ __forceinline__ void store8(void* base, long long row, int d, int l, uint32_t w, uint32_t scale,
+                                       uint32_t bits) {
+  if constexpr (F32) {
+    const float s = __uint_as_float(scale << 16), m = __uint_as_float(scale & 0xffff0000u);
+    float x[8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) x[n] = fmaf(__uint_as_float(pick<15u>(w >> (4 * n), bits)) - 8388608.f, s, m);
     float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + row * d) + 2 * l;
     p[0] = make_float4(x[0], x[1], x[2], x[3]);
     p[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    const uint32_t s2 = __byte_perm(scale, 0, 0x1010), m2 = __byte_perm(scale, 0, 0x3232);
+    uint32_t v[4];  // channels n and n + 4
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const uint32_t c = pick<0x000f000fu>(w >> (4 * n), bits);
+      uint32_t e;
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(e) : "r"(c), "r"(bits));
+      asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[n]) : "r"(e), "r"(s2), "r"(m2));
+    }
+    reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + row * d)[l] =
+        make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                   __byte_perm(v[2], v[3], 0x7632));
   }
-};
+}
 
 constexpr int kMoveWarps = 8;
 
@@ -501,14 +517,20 @@ struct StoreArgs {
 };
 
 // Warps take runs of units of 16 tokens (a unit starts at a multiple of 16 of
-// the row's tokens, so it lies in one page). D / 8 lanes hold a token's row, 8
-// channels each; a unit is quantised into shared memory in the page's layout
-// and written with 16-byte stores (each of its four parts is contiguous).
+// the row's tokens, so it lies in one page). D / 16 lanes hold a token's row, 16
+// channels each (so that a group's scale, worked out in each of its lanes, is
+// shared by 16 channels). A unit's K, then its V, is quantised into shared
+// memory in the page's layout and written with 16-byte stores (each part of a
+// unit is contiguous), while the next part's loads are under way.
+//
+// What bounds it: 2 d element bytes read and d / 2 + 4 G written a token and
+// operand, and about 10 instructions a channel, which at that rate of bytes
+// fill the SMs' issue slots as well.
 template <int D, int QG, bool F32>
 __global__ void __launch_bounds__(kMoveWarps * 32) paged_store_kernel(const StoreArgs a) {
-  constexpr int G = D / QG, LT = D / 8, TPI = 32 / LT, ITER = kUnit / TPI, W = D / 32;
+  constexpr int G = D / QG, LT = D / 16, TPI = 32 / LT, ITER = kUnit / TPI, W = D / 32, LG = QG / 16;
   constexpr int kCode = kUnit * D / 2, kScale = kUnit * G * 4;
-  __shared__ __align__(16) uint8_t stage[kMoveWarps][2 * (kCode + kScale)];
+  __shared__ __align__(16) uint8_t stage[kMoveWarps][kCode + kScale];
   const PageGeom& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane % LT, sub = lane / LT;
@@ -522,83 +544,100 @@ __global__ void __launch_bounds__(kMoveWarps * 32) paged_store_kernel(const Stor
   uint8_t* st = stage[warp];
   int row = find_unit_row(a.unit, n_rows, u0);
   int bad = 0;
-  for (int u = u0; u < u1; ++u) {
+
+  // A unit: where it goes (page, place of its first token, its new tokens [f, e)) and, in lane t, the source row of
+  // its token t (-1: none).
+  struct Unit {
+    int page, place, f, e;
+    long long src;
+  };
+  auto unit_at = [&](int u) {
+    Unit x;
     if (u >= a.unit[row + 1]) row = find_unit_row(a.unit, n_rows, u);
     const RowPlan p = a.plan[row];
     const int trow = table_row(a.rows, row);
-    const int pos0 = (p.old / kUnit + u - a.unit[row]) * kUnit;     // first token of the unit
-    const int t0 = max(pos0, p.old), t1 = min(pos0 + kUnit, p.old + p.n);  // its tokens that are new
-    const int j = pos0 >> g.log_p, place = pos0 & (g.P - 1);
-    int page;
+    const int pos0 = (p.old / kUnit + u - a.unit[row]) * kUnit;
+    x.f = max(p.old - pos0, 0);
+    x.e = min(kUnit, p.old + p.n - pos0);
+    const int j = pos0 >> g.log_p;
+    x.place = pos0 & (g.P - 1);
     if (j >= p.fresh) {
-      page = a.take[p.take + j - p.fresh];
-      if (place == 0 && lane == 0) claim_page(a.c, g, trow, j, page);
+      x.page = a.take[p.take + j - p.fresh];
+      if (x.place == 0 && lane == 0) claim_page(a.c, g, trow, j, x.page);
     } else {
-      page = a.c.table[(size_t)trow * g.max_pages + j];
+      x.page = a.c.table[(size_t)trow * g.max_pages + j];
+      if (x.page < 0 || x.page >= g.n_pages) {
+        bad |= KV_DEV_BOUNDS;
+        x.f = x.e = 0;  // nothing of it is stored
+        x.page = 0;
+      }
     }
-    // source rows: lane t holds that of token pos0 + t
-    long long src = -1;
-    if (lane < kUnit && pos0 + lane >= t0 && pos0 + lane < t1) {
+    x.src = -1;
+    if (lane >= x.f && lane < x.e) {
       const int t = pos0 + lane - p.old;
       const long long base = a.src_off ? a.src_off[row] : (long long)row * a.n_each;
-      src = base + (a.idx ? (long long)a.idx[a.idx_off[row] + t] : (long long)t);
-      if (src < 0 || src >= a.n_src) {
-        src = -1;
+      x.src = base + (a.idx ? (long long)a.idx[a.idx_off[row] + t] : (long long)t);
+      if (x.src < 0 || x.src >= a.n_src) {
+        x.src = -1;
         bad |= KV_DEV_RANGE;
       }
     }
-    if (page < 0 || page >= g.n_pages) {  // the same in every lane
-      bad |= KV_DEV_BOUNDS;
-      continue;
-    }
-    Row8<F32> k[ITER], v[ITER];
+    return x;
+  };
+  Row16<F32> cur[ITER], nxt[ITER];
+  auto load = [&](Row16<F32>(&r)[ITER], const void* from, long long src) {
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
       const long long s = __shfl_sync(0xffffffffu, src, it * TPI + sub);
-      if (s >= 0) {
-        k[it].load(a.K, s, D, l);
-        v[it].load(a.V, s, D, l);
-      } else {
-        k[it].zero();
-        v[it].zero();
-      }
+      if (s >= 0) r[it].load(from, s, D, l);
+      else r[it].zero();
     }
-    __syncwarp();  // the previous unit has left the stage
+  };
+
+  Unit now = unit_at(u0);
+  load(cur, a.K, now.src);
+#pragma unroll 1
+  for (int i = 2 * u0; i < 2 * u1; ++i) {
+    const bool v = i & 1;  // the unit's V, else its K
+    const Unit here = now;
+    if (!v) {
+      load(nxt, a.V, now.src);
+    } else if (i + 1 < 2 * u1) {
+      now = unit_at((i + 1) >> 1);
+      load(nxt, a.K, now.src);
+    }
+    __syncwarp();  // the previous part has left the stage
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
       const int t = it * TPI + sub;
-      float x[8];
-      uint32_t sc;
-      k[it].get(x);
-      uint32_t code = k[it].template quantise<QG / 8>(x, &sc);
-      reinterpret_cast<uint32_t*>(st)[t * (D / 8) + (l & 3) * W + (l >> 2)] = code;
-      if (l % (QG / 8) == 0) reinterpret_cast<uint32_t*>(st + 2 * kCode)[t * G + l / (QG / 8)] = sc;
-      v[it].get(x);
-      code = v[it].template quantise<QG / 8>(x, &sc);
-      const int pv = (2 * (l & 3)) ^ ((t & 2) << 1);  // place of channels 8 l .. 8 l + 3; the next four follow
-      uint16_t* sv = reinterpret_cast<uint16_t*>(st + kCode) + t * (D / 4) + pv * W + (l >> 2);
-      sv[0] = (uint16_t)code;
-      sv[W] = (uint16_t)(code >> 16);
-      if (l % (QG / 8) == 0) reinterpret_cast<uint32_t*>(st + 2 * kCode + kScale)[t * G + l / (QG / 8)] = sc;
+      uint32_t code[2], sc;
+      cur[it].template quantise<LG>(code, &sc);
+      // channels 16 l .. 16 l + 15 lie in channels 32 (l / 2) .. of the row, from its first or second half on
+      if (!v) {  // words (t, w), t = channel % 32 / 8
+        uint32_t* sk = reinterpret_cast<uint32_t*>(st) + t * (D / 8) + 2 * (l & 1) * W + (l >> 1);
+        sk[0] = code[0];
+        sk[W] = code[1];
+      } else {  // 16-bit words (p, h), p = channel % 32 / 4, in places swapped by the token's bit 1
+        const int p = (4 * (l & 1)) ^ ((t & 2) << 1);
+        uint16_t* sv = reinterpret_cast<uint16_t*>(st) + t * (D / 4) + p * W + (l >> 1);
+        sv[0] = (uint16_t)code[0];
+        sv[W] = (uint16_t)(code[0] >> 16);
+        sv[2 * W] = (uint16_t)code[1];
+        sv[3 * W] = (uint16_t)(code[1] >> 16);
+      }
+      if (l % LG == 0) reinterpret_cast<uint32_t*>(st + kCode)[t * G + l / LG] = sc;
     }
     __syncwarp();
-    uint8_t* pg = a.c.pages + (size_t)page * g.bytes;
-    const int f = t0 - pos0, e = t1 - pos0;  // tokens [f, e) of the unit
-    constexpr int RC = D / 2 / 16;           // 16-byte pieces of a token's codes
-    const uint4* sk = reinterpret_cast<const uint4*>(st);
-    uint4* dk = reinterpret_cast<uint4*>(pg + place * (D / 2));
-    uint4* dv = reinterpret_cast<uint4*>(pg + g.v + place * (D / 2));
-    for (int i = f * RC + lane; i < e * RC; i += 32) {
-      dk[i] = sk[i];
-      dv[i] = sk[i + kCode / 16];
-    }
-    const uint32_t* ss = reinterpret_cast<const uint32_t*>(st + 2 * kCode);
-    uint32_t* dks = reinterpret_cast<uint32_t*>(pg + g.ks) + place * G;
-    uint32_t* dvs = reinterpret_cast<uint32_t*>(pg + g.vs) + place * G;
-    for (int i = f * G + lane; i < e * G; i += 32) {
-      dks[i] = ss[i];
-      dvs[i] = ss[i + kScale / 4];
-    }
+    uint8_t* pg = a.c.pages + (size_t)here.page * g.bytes;
+    constexpr int RC = D / 2 / 16;  // 16-byte pieces of a token's codes
+    const uint4* ss = reinterpret_cast<const uint4*>(st);
+    uint4* d = reinterpret_cast<uint4*>(pg + (v ? g.v : 0) + here.place * (D / 2));
+    for (int x = here.f * RC + lane; x < here.e * RC; x += 32) d[x] = ss[x];
+    const uint32_t* sx = reinterpret_cast<const uint32_t*>(st + kCode);
+    uint32_t* dx = reinterpret_cast<uint32_t*>(pg + (v ? g.vs : g.ks)) + here.place * G;
+    for (int x = here.f * G + lane; x < here.e * G; x += 32) dx[x] = sx[x];
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) cur[it] = nxt[it];
   }
   if (bad) atomicOr(a.c.status, bad);
 }
@@ -612,11 +651,12 @@ struct LoadArgs {
   long long n_out;
   void* K;
   void* V;
+  uint32_t bits;  // see store8
 };
 
 // Warps take runs of 16 output rows; lane t finds the token of output row t.
 template <int D, int QG, bool F32>
-__global__ void __launch_bounds__(kMoveWarps * 32) paged_load_kernel(const LoadArgs a) {
+__global__ void __launch_bounds__(kMoveWarps * 32, 4) paged_load_kernel(const LoadArgs a) {
   constexpr int G = D / QG, LT = D / 8, TPI = 32 / LT, ITER = kUnit / TPI, W = D / 32;
   const PageGeom& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -683,11 +723,8 @@ __global__ void __launch_bounds__(kMoveWarps * 32) paged_load_kernel(const LoadA
     for (int it = 0; it < ITER; ++it) {
       if (!have[it]) continue;
       const long long orow = o0 + it * TPI + sub;
-      float x[8];
-      dequantise8(kc[it], ksc[it], x);
-      Row8<F32>::store(a.K, orow, D, l, x);
-      dequantise8(vc[it], vsc[it], x);
-      Row8<F32>::store(a.V, orow, D, l, x);
+      store8<F32>(a.K, orow, D, l, kc[it], ksc[it], a.bits);
+      store8<F32>(a.V, orow, D, l, vc[it], vsc[it], a.bits);
     }
   }
   if (bad) atomicOr(a.c.status, bad);
@@ -1047,7 +1084,7 @@ int kv_paged_append(const kv_paged_shape* shape, const kv_paged_cache* cache, co
   StoreArgs a = {p.g, p.dst, p.c, K, V, n_src, n_each, src_off, idx, idx_off, w.plan, w.unit, w.take};
   // a unit per warp while that leaves SMs idle; the batch's units are known on the device only, n_src bounds them
   const long long warps = n_src / kUnit + 2ll * p.dst.n_rows;
-  const long long want = (warps + kMoveWarps - 1) / kMoveWarps, cap = 4ll * sm_count();
+  const long long want = (warps + kMoveWarps - 1) / kMoveWarps, cap = 2ll * sm_count();  // all resident
   const int grid = (int)(want < cap ? want : cap);
   const bool f32 = shape->dtype == KV_F32;
   if (shape->head_dim == 64) return shape->quant_group == 32 ? store_as<64, 32>(f32, grid, a, st) : store_as<64, 64>(f32, grid, a, st);
@@ -1069,7 +1106,8 @@ int kv_paged_load(const kv_paged_shape* shape, const kv_paged_cache* cache, cons
   a.g = page_geom(*shape);
   a.c = cache_of(*cache);
   a.out_off = out_off, a.n_out = n_out, a.K = K_out, a.V = V_out;
-  const long long want = (n_out / kUnit + kMoveWarps) / kMoveWarps, cap = 8ll * sm_count();
+  a.bits = shape->dtype == KV_F32 ? 0x4B000000u : 0x43004300u;
+  const long long want = (n_out / kUnit + kMoveWarps) / kMoveWarps, cap = 4ll * sm_count();  // all resident
   const int grid = (int)(want < cap ? want : cap);
   const bool f32 = shape->dtype == KV_F32;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
