@@ -277,21 +277,33 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 __device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 __device__ __forceinline__ uint32_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
-// The code of x by its definition, in float64: the quotient's rounding does
-// not reach a half (x, m and s have at most 24, 8 and 8 bits).
-__device__ __forceinline__ uint32_t code_exact(float x, float m, float s) {
-  const double q = ((double)x - (double)m) / (double)s;
-  return (uint32_t)rint(fmin(fmax(q, 0.0), 15.0));
+// What a lane holds of a quantised group: the codes of its 16 channels,
+// channel 8 i + n in bits 4 n of w[i], and the packed (s, m).
+struct Quantised {
+  uint32_t w[2], scale;
+};
+
+// The same by the definition, in float64: the quotient's rounding does not
+// reach a half (x, m and s have at most 24, 8 and 8 bits). A call, so that the
+// common path keeps its registers and its place in the instruction cache.
+__device__ __noinline__ Quantised quantise_exact(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
+                                                 float x7, float x8, float x9, float x10, float x11, float x12,
+                                                 float x13, float x14, float x15, float mx, float m) {
+  Quantised r;
+  r.w[0] = r.w[1] = 0u;
+  r.scale = 0x7fff7fffu;  // (NaN, NaN)
+  if (!(fabsf(mx) < INFINITY && fabsf(m) < INFINITY)) return r;
+  const float s = mx > m ? bf16_round((float)(((double)mx - (double)m) / 15.0)) : 0.f;
+  r.scale = bf16_bits(s) | (__float_as_uint(m) & 0xffff0000u);
+  if (s == 0.f) return r;
+  const float x[16] = {x0, x1, x2, x3, x4, x5, x6, x7, x8, x9, x10, x11, x12, x13, x14, x15};
+#pragma unroll
+  for (int n = 0; n < 16; ++n) {
+    const double q = ((double)x[n] - (double)m) / (double)s;
+    r.w[n >> 3] |= (uint32_t)rint(fmin(fmax(q, 0.0), 15.0)) << (4 * (n & 7));
+  }
+  return r;
 }
-// Eight of them (a call: the common path keeps its registers and its place in the instruction cache).
-__device__ __noinline__ uint32_t codes_exact(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
-                                             float x7, float m, float s) {
-  uint32_t w = code_exact(x0, m, s) | code_exact(x1, m, s) << 4 | code_exact(x2, m, s) << 8;
-  w |= code_exact(x3, m, s) << 12 | code_exact(x4, m, s) << 16 | code_exact(x5, m, s) << 20;
-  return w | code_exact(x6, m, s) << 24 | code_exact(x7, m, s) << 28;
-}
-// float32 of (mx - m) / 15, taken in float64.
-__device__ __noinline__ float step_exact(float mx, float m) { return (float)(((double)mx - (double)m) / 15.0); }
 
 // Two float32 in one register pair, and the packed operations on them.
 __device__ __forceinline__ uint64_t f2(float a, float b) {
@@ -318,78 +330,73 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// Codes of the 16 channels that a lane holds of a group with largest value mx
-// and base m (bf16 of the smallest): channels 8 i + n in bits 4 n of w[i];
-// *scale the packed (s, m). All of it is exact arithmetic's result. The step:
-// the float32 product is off by a few of its last bits, so where it lies next
-// to the middle of two bf16 the quotient is taken in float64. The codes: x - m
-// is exact in float32 unless the two lie far apart, and q = RN((x - m) / s)
-// follows from the rounded reciprocal by one correction with the exact
-// remainder; it is a half only if the exact quotient is (one that is not
-// differs from a half by the last bit of x - m over s at least, more than half
-// the last bit of q). Where x - m was rounded (bf16: rare; F32: mostly, then
-// only a quotient within 1e-5 of a half matters) the codes are taken in float64.
+// Quantises the 16 channels that a lane holds of a group with largest value mx
+// and base m (bf16 of the smallest), to exact arithmetic's result. The step:
+// the float32 product is off by a few of its last bits, which matters next to
+// the middle of two bf16. The codes: x - m is exact in float32 unless the two
+// lie far apart, and q follows from a reciprocal by one correction with the
+// exact remainder. An exact quotient k + 1/2 comes out as that; another
+// differs from it by the last bit of x - m over s at least, which is more than
+// half the last bit of q by 1 part in 255 (s has 8 bits), so it comes out on
+// its own side. What this does not cover goes to quantise_exact: a step next to
+// a middle, tiny, zero or not finite; an x - m that was rounded (bf16: rare;
+// F32: mostly, then only a quotient within 1e-5 of a half matters).
 template <bool F32>
-__device__ __forceinline__ void codes_of(const float (&x)[16], float mx, float m, uint32_t (&w)[2], uint32_t* scale) {
-  w[0] = w[1] = 0u;
-  if (!(fabsf(mx) < INFINITY && fabsf(m) < INFINITY)) {
-    *scale = 0x7fff7fffu;  // (NaN, NaN)
-    return;
-  }
-  float s = 0.f;
-  if (mx > m) {
-    float f = __fmul_rn(__fsub_rn(mx, m), 1.f / 15.f);
-    const uint32_t low = __float_as_uint(f) & 0xffffu;
-    if (low - 0x7fe0u <= 0x40u || !(f > 1e-30f) || !(f < 1e37f)) f = step_exact(mx, m);
-    s = bf16_round(f);
-  }
-  *scale = bf16_bits(s) | (__float_as_uint(m) & 0xffff0000u);
-  if (s == 0.f) return;
-  bool exact = false;
-  if (s > 1e-30f) {
-    const float magic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits of the sum
-    const float r = __frcp_rn(s);
-    const uint64_t m2 = f2(m, m), nm2 = f2(-m, -m), r2 = f2(r, r), ns2 = f2(-s, -s), g2 = f2(magic, magic),
-                   n1 = f2(-1.f, -1.f);
-    uint32_t off = 0;
-    float dev = 0.f;
+__device__ __forceinline__ Quantised quantise_fast(const float (&x)[16], float mx, float m) {
+  Quantised res;
+  const float magic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits of the sum
+  const float f = __fmul_rn(__fsub_rn(mx, m), 1.f / 15.f);
+  const float s = bf16_round(f);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  const uint64_t m2 = f2(m, m), nm2 = f2(-m, -m), r2 = f2(r, r), ns2 = f2(-s, -s), g2 = f2(magic, magic),
+                 n1 = f2(-1.f, -1.f);
+  uint32_t off = 0;
+  float dev = 0.f;
+  res.w[0] = res.w[1] = 0u;
 #pragma unroll
-    for (int n = 14; n >= 0; n -= 2) {
-      const uint64_t v = f2(x[n], x[n + 1]);
-      const uint64_t t = add2(v, nm2);
-      const uint64_t q0 = mul2(t, r2);
-      uint64_t q = fma2(fma2(q0, ns2, t), r2, q0);
-      if (F32) {  // the base may be above the smallest
-        float a, b;
-        unpack2(q, a, b);
-        q = f2(fmaxf(a, 0.f), fmaxf(b, 0.f));
-      }
-      const uint64_t y = add2(q, g2);
-      float y0, y1, e0, e1;
-      unpack2(y, y0, y1);
-      if (F32) {
-        float a, b;
-        unpack2(fma2(add2(y, f2(-magic, -magic)), n1, q), a, b);
-        dev = fmaxf(dev, fmaxf(fabsf(a), fabsf(b)));
-      }
-      unpack2(fma2(v, n1, add2(t, m2)), e0, e1);  // 0 where t is exact
-      off |= __float_as_uint(e0) | __float_as_uint(e1);
-      w[n >> 3] = (w[n >> 3] << 4) + __float_as_uint(y1);
-      w[n >> 3] = (w[n >> 3] << 4) + __float_as_uint(y0);
+  for (int n = 14; n >= 0; n -= 2) {
+    const uint64_t v = f2(x[n], x[n + 1]);
+    const uint64_t t = add2(v, nm2);
+    const uint64_t q0 = mul2(t, r2);
+    uint64_t q = fma2(fma2(q0, ns2, t), r2, q0);
+    if (F32) {  // the base may be above the smallest
+      float a, b;
+      unpack2(q, a, b);
+      q = f2(fmaxf(a, 0.f), fmaxf(b, 0.f));
     }
-    w[0] -= 0x3F400000u;  // what the eight shifted exponents of `magic` (0x4B400000) add up to
-    w[1] -= 0x3F400000u;
-    exact = (off & 0x7fffffffu) == 0u || (F32 && dev <= 0.49999f);
+    const uint64_t y = add2(q, g2);
+    float y0, y1, e0, e1;
+    unpack2(y, y0, y1);
+    if (F32) {
+      float a, b;
+      unpack2(fma2(add2(y, f2(-magic, -magic)), n1, q), a, b);
+      dev = fmaxf(dev, fmaxf(fabsf(a), fabsf(b)));
+    }
+    unpack2(fma2(v, n1, add2(t, m2)), e0, e1);  // 0 where t is exact
+    off |= __float_as_uint(e0) | __float_as_uint(e1);
+    res.w[n >> 3] = (res.w[n >> 3] << 4) + __float_as_uint(y1);
+    res.w[n >> 3] = (res.w[n >> 3] << 4) + __float_as_uint(y0);
   }
-  if (!exact) {
-    w[0] = codes_exact(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], m, s);
-    w[1] = codes_exact(x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15], m, s);
-  }
+  res.w[0] -= 0x3F400000u;  // what the eight shifted exponents of `magic` (0x4B400000) add up to
+  res.w[1] -= 0x3F400000u;
+  res.scale = bf16_bits(f) | (__float_as_uint(m) & 0xffff0000u);
+  const bool covered = f > 1e-30f && f < 1e37f && (__float_as_uint(f) & 0xffffu) - 0x7fe0u > 0x40u &&
+                       ((off & 0x7fffffffu) == 0u || (F32 && dev <= 0.49999f));
+  if (!covered)
+    res = quantise_exact(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], x[8], x[9], x[10], x[11], x[12], x[13], x[14],
+                         x[15], mx, m);
+  return res;
 }
 
 __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -408,23 +415,22 @@ struct Row16<false> {
   }
   __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
   template <int LG>
-  __device__ __forceinline__ void quantise(uint32_t (&w)[2], uint32_t* scale) const {
+  __device__ __forceinline__ Quantised quantise() const {
     const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const uint32_t neg = 0x80008000u;
-    uint32_t hi = u[0], lo = u[0] ^ neg;
+    uint32_t hi = u[0], lo = u[0];
     float x[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       hi = max2_nan(hi, u[i]);
-      lo = max2_nan(lo, u[i] ^ neg);
+      lo = min2_nan(lo, u[i]);
       x[2 * i] = __uint_as_float(u[i] << 16);
       x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
-    // the largest and the negated smallest share a register
+    lo ^= 0x80008000u;  // the largest and the negated smallest share a register
     uint32_t v = max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
 #pragma unroll
     for (int o = 1; o < LG; o <<= 1) v = max2_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-    codes_of<false>(x, __uint_as_float(v << 16), __uint_as_float((v & 0xffff0000u) ^ 0x80000000u), w, scale);
+    return quantise_fast<false>(x, __uint_as_float(v << 16), __uint_as_float((v & 0xffff0000u) ^ 0x80000000u));
   }
 };
 template <>
@@ -440,7 +446,7 @@ struct Row16<true> {
     for (int i = 0; i < 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   template <int LG>
-  __device__ __forceinline__ void quantise(uint32_t (&w)[2], uint32_t* scale) const {
+  __device__ __forceinline__ Quantised quantise() const {
     float x[16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[4 * i] = v[i].x, x[4 * i + 1] = v[i].y, x[4 * i + 2] = v[i].z, x[4 * i + 3] = v[i].w;
@@ -455,7 +461,7 @@ struct Row16<true> {
       mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
     }
-    codes_of<true>(x, mx, bf16_round(mn), w, scale);
+    return quantise_fast<true>(x, mx, bf16_round(mn));
   }
 };
 
@@ -521,13 +527,13 @@ struct StoreArgs {
 // channels each (so that a group's scale, worked out in each of its lanes, is
 // shared by 16 channels). A unit's K, then its V, is quantised into shared
 // memory in the page's layout and written with 16-byte stores (each part of a
-// unit is contiguous), while the next part's loads are under way.
+// unit is contiguous).
 //
 // What bounds it: 2 d element bytes read and d / 2 + 4 G written a token and
 // operand, and about 10 instructions a channel, which at that rate of bytes
 // fill the SMs' issue slots as well.
 template <int D, int QG, bool F32>
-__global__ void __launch_bounds__(kMoveWarps * 32) paged_store_kernel(const StoreArgs a) {
+__global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 3) paged_store_kernel(const StoreArgs a) {
   constexpr int G = D / QG, LT = D / 16, TPI = 32 / LT, ITER = kUnit / TPI, W = D / 32, LG = QG / 16;
   constexpr int kCode = kUnit * D / 2, kScale = kUnit * G * 4;
   __shared__ __align__(16) uint8_t stage[kMoveWarps][kCode + kScale];
@@ -584,7 +590,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) paged_store_kernel(const Stor
     }
     return x;
   };
-  Row16<F32> cur[ITER], nxt[ITER];
+  Row16<F32> cur[ITER];
   auto load = [&](Row16<F32>(&r)[ITER], const void* from, long long src) {
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
@@ -595,37 +601,31 @@ __global__ void __launch_bounds__(kMoveWarps * 32) paged_store_kernel(const Stor
   };
 
   Unit now = unit_at(u0);
-  load(cur, a.K, now.src);
 #pragma unroll 1
   for (int i = 2 * u0; i < 2 * u1; ++i) {
     const bool v = i & 1;  // the unit's V, else its K
+    if (!v && i > 2 * u0) now = unit_at(i >> 1);
     const Unit here = now;
-    if (!v) {
-      load(nxt, a.V, now.src);
-    } else if (i + 1 < 2 * u1) {
-      now = unit_at((i + 1) >> 1);
-      load(nxt, a.K, now.src);
-    }
+    load(cur, v ? a.V : a.K, now.src);
     __syncwarp();  // the previous part has left the stage
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
       const int t = it * TPI + sub;
-      uint32_t code[2], sc;
-      cur[it].template quantise<LG>(code, &sc);
+      const Quantised z = cur[it].template quantise<LG>();
       // channels 16 l .. 16 l + 15 lie in channels 32 (l / 2) .. of the row, from its first or second half on
       if (!v) {  // words (t, w), t = channel % 32 / 8
         uint32_t* sk = reinterpret_cast<uint32_t*>(st) + t * (D / 8) + 2 * (l & 1) * W + (l >> 1);
-        sk[0] = code[0];
-        sk[W] = code[1];
+        sk[0] = z.w[0];
+        sk[W] = z.w[1];
       } else {  // 16-bit words (p, h), p = channel % 32 / 4, in places swapped by the token's bit 1
         const int p = (4 * (l & 1)) ^ ((t & 2) << 1);
         uint16_t* sv = reinterpret_cast<uint16_t*>(st) + t * (D / 4) + p * W + (l >> 1);
-        sv[0] = (uint16_t)code[0];
-        sv[W] = (uint16_t)(code[0] >> 16);
-        sv[2 * W] = (uint16_t)code[1];
-        sv[3 * W] = (uint16_t)(code[1] >> 16);
+        sv[0] = (uint16_t)z.w[0];
+        sv[W] = (uint16_t)(z.w[0] >> 16);
+        sv[2 * W] = (uint16_t)z.w[1];
+        sv[3 * W] = (uint16_t)(z.w[1] >> 16);
       }
-      if (l % LG == 0) reinterpret_cast<uint32_t*>(st + kCode)[t * G + l / LG] = sc;
+      if (l % LG == 0) reinterpret_cast<uint32_t*>(st + kCode)[t * G + l / LG] = z.scale;
     }
     __syncwarp();
     uint8_t* pg = a.c.pages + (size_t)here.page * g.bytes;
@@ -636,8 +636,6 @@ __global__ void __launch_bounds__(kMoveWarps * 32) paged_store_kernel(const Stor
     const uint32_t* sx = reinterpret_cast<const uint32_t*>(st + kCode);
     uint32_t* dx = reinterpret_cast<uint32_t*>(pg + (v ? g.vs : g.ks)) + here.place * G;
     for (int x = here.f * G + lane; x < here.e * G; x += 32) dx[x] = sx[x];
-#pragma unroll
-    for (int it = 0; it < ITER; ++it) cur[it] = nxt[it];
   }
   if (bad) atomicOr(a.c.status, bad);
 }
@@ -1084,7 +1082,7 @@ int kv_paged_append(const kv_paged_shape* shape, const kv_paged_cache* cache, co
   StoreArgs a = {p.g, p.dst, p.c, K, V, n_src, n_each, src_off, idx, idx_off, w.plan, w.unit, w.take};
   // a unit per warp while that leaves SMs idle; the batch's units are known on the device only, n_src bounds them
   const long long warps = n_src / kUnit + 2ll * p.dst.n_rows;
-  const long long want = (warps + kMoveWarps - 1) / kMoveWarps, cap = 2ll * sm_count();  // all resident
+  const long long want = (warps + kMoveWarps - 1) / kMoveWarps, cap = 3ll * sm_count();  // all resident
   const int grid = (int)(want < cap ? want : cap);
   const bool f32 = shape->dtype == KV_F32;
   if (shape->head_dim == 64) return shape->quant_group == 32 ? store_as<64, 32>(f32, grid, a, st) : store_as<64, 64>(f32, grid, a, st);
