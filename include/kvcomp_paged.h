@@ -89,8 +89,8 @@ typedef struct {
   int32_t* ref;        /* [n_pages]                                           */
   uint32_t* free_bits; /* [ceil(n_pages / 32)]                                */
   int32_t* status;     /* device status word (KV_DEV_* bits are OR-ed in)     */
-  void* ws;            /* kv_paged_ws_bytes() bytes; contents do not matter   */
-  size_t ws_bytes;     /*   between calls                                     */
+  void* ws;            /* kv_paged_ws_bytes() bytes, prepared by              */
+  size_t ws_bytes;     /*   kv_paged_rebuild (or zeroed) before its first use */
 } kv_paged_cache;
 
 /* Bytes of a page, or 0 on a bad shape. */
@@ -100,9 +100,9 @@ size_t kv_paged_page_bytes(const kv_paged_shape* shape);
 size_t kv_paged_ws_bytes(const kv_paged_shape* shape);
 
 /*
- * kv_paged_rebuild — ref and free_bits from table and len: what a cache needs
- * before its first call (with len = 0 it is empty) and after its state was
- * loaded from elsewhere. Page numbers outside the pool set KV_DEV_BOUNDS.
+ * kv_paged_rebuild — ref and free_bits from table and len, and the workspace:
+ * what a cache needs before its first call (with len = 0 it is empty) and after
+ * its state was loaded from elsewhere. Page numbers outside the pool set KV_DEV_BOUNDS.
  * Errors: KV_ERR_ARG, KV_ERR_WORKSPACE, KV_ERR_CUDA.
  */
 int kv_paged_rebuild(const kv_paged_shape* shape, const kv_paged_cache* cache, void* stream);

@@ -53,13 +53,15 @@ static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 PagedWs paged_ws_layout(const kv_paged_shape& sh) {
   const size_t rows = (size_t)(sh.n_seqs < KV_MAX_SEQ ? sh.n_seqs : KV_MAX_SEQ) * sh.n_layers * sh.n_kv_heads;
   PagedWs w;
-  w.plan = 0;
+  w.arrived = 0;
+  w.arrived_bytes =
+      ((size_t)sm_count() * kAttnCtasPerSm * 2 + (KV_PAGED_MAX_QUERIES / 8) * kAttnRows) * sizeof(int);
+  w.part = align256(w.arrived + w.arrived_bytes);
+  // two partials per attention CTA: (max, sum) and the output of up to kAttnQ query rows
+  w.plan = align256(w.part + (size_t)sm_count() * kAttnCtasPerSm * 2 * kAttnQ * (sh.head_dim + 2) * sizeof(float));
   w.unit = align256(w.plan + rows * sizeof(RowPlan));
   w.take = align256(w.unit + (rows + 1) * sizeof(int));
-  w.att_base = align256(w.take + (size_t)sh.n_pages * sizeof(int));
-  w.part = align256(w.att_base + (size_t)sm_count() * kAttnCtasPerSm * 4 * sizeof(int));
-  // two partials per attention CTA: (max, sum) and the output of up to kAttnQ query rows
-  w.bytes = align256(w.part + (size_t)sm_count() * kAttnCtasPerSm * 2 * kAttnQ * (sh.head_dim + 2) * sizeof(float));
+  w.bytes = align256(w.take + (size_t)sh.n_pages * sizeof(int));
   return w;
 }
 
@@ -1050,7 +1052,10 @@ int kv_paged_rebuild(const kv_paged_shape* shape, const kv_paged_cache* cache, v
   const PageGeom g = page_geom(*shape);
   const PagedCache c = cache_of(*cache);
   const int rows = shape->n_seqs * shape->n_layers * shape->n_kv_heads;
-  if (cudaMemsetAsync(c.ref, 0, (size_t)g.n_pages * sizeof(int32_t), st) != cudaSuccess) return KV_ERR_CUDA;
+  const PagedWs w = paged_ws_layout(*shape);
+  if (cudaMemsetAsync(c.ref, 0, (size_t)g.n_pages * sizeof(int32_t), st) != cudaSuccess ||
+      cudaMemsetAsync(static_cast<uint8_t*>(cache->ws) + w.arrived, 0, w.arrived_bytes, st) != cudaSuccess)
+    return KV_ERR_CUDA;
   const int cap = sm_count() * 8;
   paged_count_kernel<<<rows < cap ? rows : cap, kRowThreads, 0, st>>>(g, rows, c);
   const int blocks = (g.n_pages + kRowThreads - 1) / kRowThreads;

@@ -29,15 +29,16 @@
 // which a tile's keys take the rows.
 //
 // Work. Rows are cut into tiles of 64 tokens; a row costs its tiles plus a
-// charge for starting and leaving it (an empty row 1).
-// The CTAs (up to three per SM) take equal shares of the total, contiguous
-// over rows; in a CTA one warp streams each row's queries and tiles into rings
-// of stages with bulk copies (the four parts of a page's 64 tokens are each
-// contiguous), running ahead over row ends, and four warps take 16 tokens of a
-// tile each, with a softmax of their own that is
-// joined when the CTA leaves the row. A row that several CTAs share leaves
-// partials, joined by paged_combine_kernel in CTA order. Every sum has a fixed
-// order.
+// charge for starting and leaving it (an empty row 1). The CTAs (up to three
+// per SM) take equal shares of the total, contiguous over rows. In a CTA one
+// warp runs ahead, over row ends too: it streams the tiles into a ring of stages
+// with bulk copies (the four parts of a page's 64 tokens are each contiguous)
+// and lays out each row's queries as matrix fragments. Four warps take 16
+// tokens of a tile each, with a softmax of their own that is joined when the
+// CTA leaves the row. CTAs that share a row leave partials: of each eight in
+// turn the one that comes last, by a counter, joins them, and of those the last
+// joins the eights (one CTA loads a partial in no less than 0.04 us, and eight
+// of them in one latency). Every sum has a fixed order.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -50,22 +51,27 @@ namespace {
 constexpr int kTile = 64;     // tokens per tile
 constexpr int kWarps = 4;     // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kStages = 5;
-constexpr int kRowCost = 2;   // of starting and leaving a row, in tiles
+constexpr int kRowCost = 4;   // of starting and leaving a row, in tiles
+constexpr int kMinShare = 4;  // cost of a CTA's share, at least
+constexpr int kJoin = 8;      // partials joined at once
 constexpr float kGrow = 8.f;  // the running maximum moves when a logit passes it by this (log2 units)
 
-// Shared memory of a CTA.
+// Shared memory of a CTA: the ring of stages, the warps' outputs and (maximum,
+// sum) on leaving a row, the rows' costs before them and lengths, two rows'
+// queries (matrix fragments; per query its sums by group and its unit).
 template <int D, int NG, int NT, bool F32>
 struct Smem {
+  static constexpr int kStages = NG == 4 ? 4 : 5;
   static constexpr int kCode = kTile * D / 2, kScale = kTile * NG * 4;
   static constexpr int kV = kCode, kKs = 2 * kCode, kVs = kKs + kScale, kStage = kVs + kScale;
   static constexpr int NQ = NT * 8, kORow = D + 4;
   static constexpr int kObuf = kStages * kStage;
   static constexpr int kMl = kObuf + kWarps * NQ * kORow * 4;
-  static constexpr int kBase = kMl + kWarps * NQ * 8;
-  static constexpr int kQ = (kBase + (kAttnRows + 1) * 4 + 15) / 16 * 16;  // two rows' queries
-  static constexpr int kQBytes = NQ * D * (F32 ? 4 : 2);
-  static constexpr int kBar = kQ + 2 * kQBytes;
+  static constexpr int kQ = kMl + kWarps * NQ * 8;
+  static constexpr int kFrag = NQ * D * (F32 ? 4 : 2), kQBytes = kFrag + NQ * (NG + 1) * 4;
+  static constexpr int kBase = kQ + 2 * kQBytes;
+  static constexpr int kLen = kBase + (kAttnRows + 1) * 4;
+  static constexpr int kBar = (kLen + kAttnRows * 4 + 7) / 8 * 8;
   static constexpr int kBytes = kBar + (2 * kStages + 4) * 8 + 48;
 };
 
@@ -131,7 +137,7 @@ struct AttnArgs {
   const void* q;
   void* out;
   float* lse;
-  int4* split;       // [CTAs]: a row whose second CTA this is (row, first CTA, last CTA), or -1
+  int* arrived;      // counters, 0 between calls: [chunks of queries][2 CTAs + kAttnRows] (see leave)
   float* part;
   unsigned long long limit_ns;
   CodeConst kc;  // an argument, so that the constants stay in registers
@@ -158,10 +164,24 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// CTAs that share the work: at least two tiles' cost each.
-__device__ __forceinline__ int cta_count(int cost, int grid) { return max(1, min(grid, (cost + 1) / 2)); }
-
 __device__ __forceinline__ int row_cost(int len) { return len > 0 ? (len + kTile - 1) / kTile + kRowCost : 1; }
+
+// Equal shares of `cost` for n CTAs: CTA c has [lo(c), lo(c + 1)), lo(c) = floor(cost c / n).
+struct Shares {
+  int n, each, rest;
+  __device__ __forceinline__ Shares(int cost, int grid) {
+    n = max(1, min(grid, cost / kMinShare));
+    each = cost / n;
+    rest = cost - each * n;
+  }
+  __device__ __forceinline__ int lo(int c) const { return each * c + rest * c / n; }
+  __device__ __forceinline__ int holder(int at) const {  // the CTA with lo(c) <= at < lo(c + 1)
+    int c = min(n - 1, (int)__fdividef((float)at * (float)n, (float)each * (float)n + (float)rest));
+    while (lo(c) > at) --c;
+    while (c + 1 < n && lo(c + 1) <= at) ++c;
+    return c;
+  }
+};
 
 // The tiles [t0, t1) of a row of cost [b0, b1) that the CTA with costs [lo, hi) takes.
 struct Share {
@@ -175,21 +195,37 @@ __device__ __forceinline__ Share share_of(int b0, int b1, int lo, int hi) {
   return s;
 }
 
+// The output of four channels of a query, o / L, in its type.
+template <bool F32>
+__device__ __forceinline__ void put4(void* out, long long at, float4 o, float L) {
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  if constexpr (F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) =
+        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
+        make_uint2(pack2_bf16(o.x * inv, o.y * inv), pack2_bf16(o.z * inv, o.w * inv));
+}
+__device__ __forceinline__ float lse_of(float M, float L) {
+  return L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
 template <int D, int NG, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2) paged_attn_kernel(const AttnArgs a) {
   using S = Smem<D, NG, NT, F32>;
-  constexpr int W = D / 32, NQ = S::NQ, PARTS = F32 ? 2 : 1;
+  constexpr int W = D / 32, NQ = S::NQ, PARTS = F32 ? 2 : 1, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   float* obuf = reinterpret_cast<float*>(smem + S::kObuf);
   float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
   int* base = reinterpret_cast<int*>(smem + S::kBase);
+  int* lens = reinterpret_cast<int*>(smem + S::kLen);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBar);
   uint64_t* empty = full + kStages;
   uint64_t* q_full = empty + kStages;  // [2], by the parity of the row's number in this CTA
   uint64_t* q_empty = q_full + 2;
-  int* wsum = reinterpret_cast<int*>(q_empty + 2);
-  int* q_len = wsum + 8;  // [2]
-  volatile int* abort_flag = wsum + 10;
+  int* wsum = reinterpret_cast<int*>(q_empty + 2);  // [5]
+  int* abort_flag = wsum + 10;
+  int* last_flag = wsum + 11;
   const PageGeom& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -219,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         n = 0;
         if (blockIdx.x == 0) atomicOr(a.c.status, KV_DEV_BOUNDS);
       }
+      lens[i] = n;
       base[i] = sum;  // made absolute below
       sum += row_cost(n);
     }
@@ -236,15 +273,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     if (i1 == a.n_rows && i0 < a.n_rows) base[a.n_rows] = before + sum;
     __syncthreads();
   }
-  const int cost = base[a.n_rows];
-  const int n_cta = cta_count(cost, gridDim.x);
-  const int cta = blockIdx.x;
-  const int chunk = blockIdx.y;  // of NQ query rows
-  if (cta >= n_cta) {
-    if (threadIdx.x == 0 && chunk == 0) a.split[cta] = make_int4(-1, 0, 0, 0);
-    return;
-  }
-  const int lo = (int)((long long)cost * cta / n_cta), hi = (int)((long long)cost * (cta + 1) / n_cta);
+  const Shares shares(base[a.n_rows], gridDim.x);
+  const int cta = blockIdx.x, chunk = blockIdx.y;  // the chunk of NQ query rows
+  if (cta >= shares.n) return;
+  const int lo = shares.lo(cta), hi = shares.lo(cta + 1);
   int row = 0;
   {
     int x = 0, y = a.n_rows - 1;  // the last row with base <= lo
@@ -255,17 +287,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     }
     row = x;
   }
-  if (threadIdx.x == 0 && chunk == 0) {
-    const int t0 = lo - base[row] - kRowCost;  // > 0: the row's first tiles are another CTA's
-    int4 rec = make_int4(-1, 0, 0, 0);
-    if (t0 > 0) {
-      const int f = (int)(((long long)(base[row] + kRowCost + 1) * n_cta - 1) / cost);  // holds the row's first tile
-      const int l = (int)(((long long)base[row + 1] * n_cta - 1) / cost);    // holds its last
-      if (f + 1 == cta) rec = make_int4(row, f, l, 0);
-    }
-    a.split[cta] = rec;
-  }
   const Guard guard{abort_flag, a.c.status, a.limit_ns};
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return (bool)__all_sync(0xffffffffu, wait_bounded(bar, parity, guard));
+  };
+  const int grp = lane >> 2, tig = lane & 3;
+  const int q0 = chunk * NQ, nq = min(NQ, a.R - q0);
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
@@ -276,31 +303,87 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     const int sec_page = sec == 0 ? 0 : sec == 1 ? g.v : sec == 2 ? g.ks : g.vs;
     const int sec_stage = sec == 0 ? 0 : sec == 1 ? S::kV : sec == 2 ? S::kKs : S::kVs;
     const uint32_t tok_bytes = sec < 2 ? D / 2 : NG * 4;
-    const int q0 = chunk * NQ, nq = min(NQ, a.R - q0);
-    constexpr int EB = F32 ? 4 : 2;
-    int it = 0, k = 0;
+    int it = 0, st = 0, k = 0;  // tiles and rows so far; the stage that is next
+    uint32_t turn = 0;          // the ring's turns, odd or even
     bool ok = true;
     for (int r = row; ok && r < a.n_rows && base[r] < hi; ++r) {
-      const auto [tiles, t0, t1] = share_of(base[r], base[r + 1], lo, hi);
-      if (t0 >= t1) continue;
-      const int trow = table_row(a.rows, a.row0 + r);
-      const int32_t* list = a.c.table + (size_t)trow * g.max_pages;
-      const int len = a.c.len[trow];
-      const int np = (len + g.P - 1) >> g.log_p;
-      if (k >= 2) ok = wait_bounded(&q_empty[k & 1], ((k >> 1) - 1) & 1, guard);
-      ok = __all_sync(0xffffffffu, ok);
+      const Share sh = share_of(base[r], base[r + 1], lo, hi);
+      if (sh.t0 >= sh.t1) continue;
+      const int32_t* list = a.c.table + (size_t)table_row(a.rows, a.row0 + r) * g.max_pages;
+      const int np = (lens[r] + g.P - 1) >> g.log_p;
+      int win = (sh.t0 * kTile) >> g.log_p;  // lane l holds page number list[win + l]
+      int entry = win + lane < np ? list[win + lane] : -1;
+      if (k >= 2) ok = wait(&q_empty[k & 1], ((k >> 1) - 1) & 1);
       if (!ok) break;
-      if (lane == 0) {
-        const uint32_t bytes = (uint32_t)(nq * D * EB);
-        q_len[k & 1] = len;
-        mbar_arrive_expect_tx(&q_full[k & 1], bytes);
-        bulk_load(smem + S::kQ + (k & 1) * S::kQBytes,
-                  static_cast<const uint8_t*>(a.q) + ((long long)(a.row0 + r) * a.R + q0) * (D * EB), bytes,
-                  &q_full[k & 1]);
+      // the row's queries: scaled by a power of two each, as fragments, with their sums by group and units
+      {
+        uint4* frag = reinterpret_cast<uint4*>(smem + S::kQ + (k & 1) * S::kQBytes);
+        float* meta = reinterpret_cast<float*>(smem + S::kQ + (k & 1) * S::kQBytes + S::kFrag);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int qi = nt * 8 + grp;
+          float x[W][8], top = 0.f, sum[NG];
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const long long at = ((long long)(a.row0 + r) * a.R + q0 + qi) * D + 32 * w + 8 * tig;
+            if (qi < nq) {
+              if (F32) {
+                const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+                const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 4);
+                x[w][0] = u.x, x[w][1] = u.y, x[w][2] = u.z, x[w][3] = u.w;
+                x[w][4] = v.x, x[w][5] = v.y, x[w][6] = v.z, x[w][7] = v.w;
+              } else {
+                const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+                x[w][0] = lo_f(u.x), x[w][1] = hi_f(u.x), x[w][2] = lo_f(u.y), x[w][3] = hi_f(u.y);
+                x[w][4] = lo_f(u.z), x[w][5] = hi_f(u.z), x[w][6] = lo_f(u.w), x[w][7] = hi_f(u.w);
+              }
+            } else {
+#pragma unroll
+              for (int n = 0; n < 8; ++n) x[w][n] = 0.f;
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int n = 0; n < 8; ++n) top = fmaxf(top, fabsf(x[w][n]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = max(-100, (int)(__float_as_uint(top) >> 23) - 127);  // 2^e <= top < 2^(e + 1)
+          const float up = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+          const float down = a.scale2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+#pragma unroll
+          for (int z = 0; z < NG; ++z) sum[z] = 0.f;
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              x[w][n] *= up;
+              sum[w * NG / W] += x[w][n];
+            }
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+              uint32_t f[4];  // a code pair holds channels n and n + 4
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                f[n] = pack2(x[w][n], x[w][n + 4]);
+                rest2(f[n], x[w][n], x[w][n + 4]);
+              }
+              frag[((nt * PARTS + p) * W + w) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+            }
+          }
+#pragma unroll
+          for (int z = 0; z < NG; ++z) {
+            sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 1);
+            sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 2);
+            if (tig == 0) meta[qi * (NG + 1) + z] = sum[z];
+          }
+          if (tig == 0) meta[qi * (NG + 1) + NG] = down;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[k & 1]);
+        ++k;
       }
-      ++k;
-      int win = -32, entry = 0;  // lane l holds page number list[win + l]
-      for (int t = t0; t < t1; ++t, ++it) {
+      for (int t = sh.t0; t < sh.t1; ++t, ++it) {
         const int j0 = (t * kTile) >> g.log_p;
         if (j0 + ppt > win + 32) {
           win = j0;
@@ -310,42 +393,43 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         const bool there = mine && j0 + pg < np;
         const bool good = there && page >= 0 && page < g.n_pages;
         if (there && !good) atomicOr(a.c.status, KV_DEV_BOUNDS);
-        const int s = it % kStages;
-        if (it >= kStages) ok = wait_bounded(&empty[s], ((it / kStages) - 1) & 1, guard);
-        ok = __all_sync(0xffffffffu, ok);
+        if (it >= kStages) ok = wait(&empty[st], (turn & 1) ^ 1);
         if (!ok) break;
         const unsigned n_good = __popc(__ballot_sync(0xffffffffu, good && sec == 0));
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], n_good * part_tokens * (D + 8 * NG));
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], n_good * part_tokens * (D + 8 * NG));
         __syncwarp();
         if (good) {
           const uint8_t* src =
               a.c.pages + (size_t)page * g.bytes + sec_page + ((t * kTile) & (g.P - 1)) * tok_bytes;
-          bulk_load(smem + s * S::kStage + sec_stage + pg * part_tokens * tok_bytes, src, sec_bytes, &full[s]);
+          bulk_load(smem + st * S::kStage + sec_stage + pg * part_tokens * tok_bytes, src, sec_bytes, &full[st]);
+        }
+        if (++st == kStages) {
+          st = 0;
+          ++turn;
         }
       }
     }
     // copies in flight land before the CTA gives its memory back, also when the others have given up
     for (int i = max(0, it - kStages); i < it; ++i) wait_drain(&full[i % kStages], (i / kStages) & 1);
-    for (int i = max(0, k - 2); i < k; ++i) wait_drain(&q_full[i & 1], (i >> 1) & 1);
     return;
   }
 
   // -------------------------------------------------------------- consumers
-  const int grp = lane >> 2, tig = lane & 3;
   const CodeConst kc = a.kc;
   // Matrix row r of a half tile is token tok(r): rows 2 t and 2 t + 1 are tokens t and 4 + (t ^ 1), so that the
   // lanes of a K load and of a V load fall on different banks.
   const int krow = warp * 16 + ((grp & 1) ? 4 + ((grp >> 1) ^ 1) : grp >> 1);
   const int vrow = warp * 16 + tig, vrow2 = warp * 16 + 4 + (tig ^ 1);
   const int vplace = grp ^ ((tig & 2) << 1);
-  const int q0 = chunk * NQ, nq = min(NQ, a.R - q0);
-  int it = 0, k = 0;
+  int st = 0, k = 0;  // the stage that is next, rows so far
+  uint32_t turn = 0;
   bool ok = true;
   for (int r = row; r < a.n_rows && base[r] < hi; ++r) {
-    const auto [tiles, t0, t1] = share_of(base[r], base[r + 1], lo, hi);
+    const Share sh = share_of(base[r], base[r + 1], lo, hi);
     const int crow = a.row0 + r;
-    if (t0 >= t1) {
-      if (tiles == 0) {  // an empty row
+    const bool whole = sh.t0 == 0 && sh.t1 == sh.tiles;
+    if (sh.t0 >= sh.t1) {
+      if (sh.tiles == 0) {  // an empty row
         const long long at = (long long)crow * a.R + q0;
         uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + at * (D * (F32 ? 4 : 2)));
         for (int i = threadIdx.x; i < nq * D * (F32 ? 4 : 2) / 16; i += kWarps * 32) o[i] = make_uint4(0, 0, 0, 0);
@@ -353,71 +437,50 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       }
       continue;
     }
-    ok = wait_bounded(&q_full[k & 1], (k >> 1) & 1, guard);
-    ok = __all_sync(0xffffffffu, ok);
-    const int len = q_len[k & 1];
-    const uint8_t* qs = smem + S::kQ + (k & 1) * S::kQBytes;
+    const int len = lens[r];
+    // CTAs that share the row (the first and the last hold its first and last tile)
+    const int c_first = whole ? cta : shares.holder(base[r] + kRowCost);
+    const int c_count = whole ? 1 : shares.holder(base[r + 1] - 1) - c_first + 1;
+    // Counts this CTA's partial of a shared row. The row's CTAs come in eights; `first`, the slot of an eight's first
+    // partial, has the eight's counter, the row counts the eights that are complete. True for the last of n.
+    int* arrived = a.arrived + chunk * (2 * gridDim.x + kAttnRows);
+    auto last_of = [&](int* counter, int n) {
+      const bool last = atomicAdd(counter, 1) == n - 1;
+      if (last) *counter = 0;
+      return last;
+    };
+    const int c_own = cta - c_first, eight = c_own / kJoin;
+    const int eights = (c_count + kJoin - 1) / kJoin, in_eight = min(kJoin, c_count - eight * kJoin);
+    const int first = eight == 0 ? 2 * c_first + 1 : 2 * (c_first + eight * kJoin);
+    if (!ok) {  // a wait ran out: the counters of the CTA's other rows stay in step all the same
+      if (!whole && threadIdx.x == 0 && last_of(arrived + first, in_eight) && eights > 1)
+        last_of(arrived + 2 * gridDim.x + r, eights);
+      continue;
+    }
+    ok = wait(&q_full[k & 1], (k >> 1) & 1);
 
     // query fragments, their sums by group, and what turns a sum into a logit in log2 units
     uint32_t qf[NT][PARTS][W][4];
     float qsum[NT][NG][2], unit[NT][2];
+    {
+      const uint4* frag = reinterpret_cast<const uint4*>(smem + S::kQ + (k & 1) * S::kQBytes);
+      const float* meta = reinterpret_cast<const float*>(smem + S::kQ + (k & 1) * S::kQBytes + S::kFrag);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int qi = nt * 8 + grp;
-      float x[W][8], top = 0.f, sum[NG];
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const int at = qi * D + 32 * w + 8 * tig;
-        if (qi < nq) {
-          if (F32) {
-            const float4 u = *reinterpret_cast<const float4*>(qs + at * 4);
-            const float4 v = *reinterpret_cast<const float4*>(qs + at * 4 + 16);
-            x[w][0] = u.x, x[w][1] = u.y, x[w][2] = u.z, x[w][3] = u.w;
-            x[w][4] = v.x, x[w][5] = v.y, x[w][6] = v.z, x[w][7] = v.w;
-          } else {
-            const uint4 u = *reinterpret_cast<const uint4*>(qs + at * 2);
-            x[w][0] = lo_f(u.x), x[w][1] = hi_f(u.x), x[w][2] = lo_f(u.y), x[w][3] = hi_f(u.y);
-            x[w][4] = lo_f(u.z), x[w][5] = hi_f(u.z), x[w][6] = lo_f(u.w), x[w][7] = hi_f(u.w);
-          }
-        } else {
-#pragma unroll
-          for (int n = 0; n < 8; ++n) x[w][n] = 0.f;
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) top = fmaxf(top, fabsf(x[w][n]));
-      }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = max(-100, (int)(__float_as_uint(top) >> 23) - 127);  // 2^e <= top < 2^(e + 1)
-      const float up = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
-      const float down = a.scale2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
-#pragma unroll
-      for (int z = 0; z < NG; ++z) sum[z] = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          x[w][n] *= up;
-          sum[w * NG / W] += x[w][n];
-        }
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {  // a code pair holds channels n and n + 4
-            qf[nt][p][w][n] = pack2(x[w][n], x[w][n + 4]);
-            rest2(qf[nt][p][w][n], x[w][n], x[w][n + 4]);
+          for (int w = 0; w < W; ++w) {
+            const uint4 u = frag[((nt * PARTS + p) * W + w) * 32 + lane];
+            qf[nt][p][w][0] = u.x, qf[nt][p][w][1] = u.y, qf[nt][p][w][2] = u.z, qf[nt][p][w][3] = u.w;
           }
-      }
 #pragma unroll
-      for (int z = 0; z < NG; ++z) {
-        sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 1);
-        sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 2);
-      }
+        for (int c = 0; c < 2; ++c) {  // this lane's columns are queries 2 tig + c
+          const float* mq = meta + (nt * 8 + 2 * tig + c) * (NG + 1);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {  // lane 4 r holds those of query r; this lane's columns are queries 2 tig + c
-#pragma unroll
-        for (int z = 0; z < NG; ++z) qsum[nt][z][c] = __shfl_sync(0xffffffffu, sum[z], (2 * tig + c) * 4);
-        unit[nt][c] = __shfl_sync(0xffffffffu, down, (2 * tig + c) * 4);
+          for (int z = 0; z < NG; ++z) qsum[nt][z][c] = mq[z];
+          unit[nt][c] = mq[NG];
+        }
       }
     }
     __syncwarp();
@@ -551,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
           const int e = max(-95, (int)(__float_as_uint(s_max) >> 23) - 127);
           const float now = __uint_as_float((uint32_t)(127 + 5 - e) << 23);
           s_top = s_max == 0.f ? 0.f : __uint_as_float((uint32_t)(127 + e + 1) << 23);
-          fo = now / om;
+          fo = now * __frcp_rn(om);
           om = now;
         }
 #pragma unroll
@@ -565,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
             const float now = fmaxf(m2[nt][x], mx * unit[nt][x]);
             const float f = now == m2[nt][x] ? 1.f : ex2_approx(m2[nt][x] - now), g2 = f * fo;
             m2[nt][x] = now;
-            thr[nt][x] = (now + kGrow) / unit[nt][x];
+            thr[nt][x] = __fdividef(now + kGrow, unit[nt][x]);
             l[nt][x] *= f;
 #pragma unroll
             for (int z = 0; z < NG; ++z) off[nt][z][x] *= f;
@@ -649,26 +712,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       }
     };
 
-    for (int t = t0; ok && t < t1;) {
+    for (int t = sh.t0; ok && t < sh.t1;) {
       // two tiles at once while every query sees all of them
-      const int n = t + 2 <= t1 && (t + 1) * kTile + warp * 16 + 16 <= lim_min ? 2 : 1;
-      const int s0 = it % kStages, s1 = (it + 1) % kStages;
-      ok = wait_bounded(&full[s0], (it / kStages) & 1, guard);
-      if (ok && n == 2) ok = wait_bounded(&full[s1], ((it + 1) / kStages) & 1, guard);
-      ok = __all_sync(0xffffffffu, ok);
+      const bool two = t + 2 <= sh.t1 && (t + 1) * kTile + warp * 16 + 16 <= lim_min;
+      const int s0 = st, s1 = st + 1 == kStages ? 0 : st + 1;
+      ok = wait(&full[s0], turn & 1);
+      if (two && ok) ok = wait(&full[s1], (turn + (s1 == 0)) & 1);
       if (!ok) break;
       const uint8_t *st0 = smem + s0 * S::kStage, *st1 = smem + s1 * S::kStage;
-      if (n == 2)
+      if (two)
         attend(std::integral_constant<int, 2>{}, st0, st1, t);
       else if (t * kTile + warp * 16 < len)
         attend(std::integral_constant<int, 1>{}, st0, st1, t);
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&empty[s0]);
-        if (n == 2) mbar_arrive(&empty[s1]);
+        if (two) mbar_arrive(&empty[s1]);
       }
+      const int n = two ? 2 : 1;
       t += n;
-      it += n;
+      st += n;
+      if (st >= kStages) {
+        st -= kStages;
+        ++turn;
+      }
     }
 
     // ---- the CTA leaves the row: the warps' sums are joined
@@ -696,9 +763,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       }
     }
     ok = named_bar_and(1, kWarps * 32, ok);
-    if (!ok) break;
-    const bool whole = t0 == 0 && t1 == tiles;
-    float* part = a.part + (size_t)((chunk * gridDim.x + cta) * 2 + (t0 == 0 ? 1 : 0)) * (kAttnQ * (D + 2));
+    if (!ok) {
+      if (!whole && threadIdx.x == 0 && last_of(arrived + first, in_eight) && eights > 1)
+        last_of(arrived + 2 * gridDim.x + r, eights);
+      continue;
+    }
+    constexpr size_t kPart = kAttnQ * (D + 2);  // floats: (max, sum) and the output of up to kAttnQ query rows
+    float* parts = a.part + (size_t)chunk * gridDim.x * 2 * kPart;
+    float* part = parts + (size_t)(cta * 2 + (c_own == 0 ? 1 : 0)) * kPart;
     for (int i = threadIdx.x; i < nq * (D / 4); i += kWarps * 32) {
       const int qi = i / (D / 4), dim = 4 * (i - qi * (D / 4));
       float M = -INFINITY, L = 0.f;
@@ -714,83 +786,78 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
       }
       if (whole) {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const long long at = ((long long)crow * a.R + q0 + qi);
-        if (F32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * D + dim) =
-              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        } else {
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * D + dim) =
-              make_uint2(pack2_bf16(o.x * inv, o.y * inv), pack2_bf16(o.z * inv, o.w * inv));
-        }
-        if (a.lse && dim == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        const long long at = (long long)crow * a.R + q0 + qi;
+        put4<F32>(a.out, at * D + dim, o, L);
+        if (a.lse && dim == 0) a.lse[at] = lse_of(M, L);
       } else {
         *reinterpret_cast<float4*>(part + 2 * kAttnQ + qi * D + dim) = o;
         if (dim == 0) reinterpret_cast<float2*>(part)[qi] = make_float2(M, L);
       }
     }
-    named_bar_sync(1, kWarps * 32);  // the buffer is free again
-  }
-}
-
-// Joins the partials of the rows that CTAs shared: block (CTA c, query) works
-// if c is the second CTA of a row. Four warps take every fourth partial.
-template <int D, bool F32>
-__global__ void __launch_bounds__(128) paged_combine_kernel(const AttnArgs a, int grid, int nq_chunk) {
-  __shared__ float4 acc[4][32];
-  __shared__ float2 red[4];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int4 rec = a.split[blockIdx.x];
-  if (rec.x < 0) return;
-  const int qa = blockIdx.y;
-  const int chunk = qa / nq_chunk, qi = qa - chunk * nq_chunk;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = rec.z - rec.y + 1;
-  const size_t stride = kAttnQ * (D + 2);
-  const float* first = a.part + (size_t)(chunk * grid + rec.y) * 2 * stride;
-  // partial k: the first CTA's second slot, then the first slot of each CTA after it
-  auto at = [&](int k) { return first + (k == 0 ? stride : (size_t)k * 2 * stride); };
-  float M = -INFINITY;
-  for (int k = threadIdx.x; k < n; k += 128) M = fmaxf(M, reinterpret_cast<const float2*>(at(k))[qi].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) red[warp].x = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(red[0].x, red[1].x), fmaxf(red[2].x, red[3].x));
-  float L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = warp; k < n; k += 4) {
-    const float* p = at(k);
-    const float2 e = reinterpret_cast<const float2*>(p)[qi];
-    const float f = e.x == M ? 1.f : ex2_approx(e.x - M);
-    L += e.y * f;
-    if (4 * lane < D) {
-      const float4 v = *reinterpret_cast<const float4*>(p + 2 * kAttnQ + qi * D + 4 * lane);
-      o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+    if (whole) {
+      named_bar_sync(1, kWarps * 32);  // the buffer is free again
+      continue;
     }
-  }
-  acc[warp][lane] = o;
-  if (lane == 0) red[warp].y = L;
-  __syncthreads();
-  if (warp == 0 && 4 * lane < D) {
-    L = (red[0].y + red[1].y) + (red[2].y + red[3].y);
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // a shared row: joins n partials, the first at slot s0 and the others at slots s1, s1 + ds, ..
+    auto join = [&](int n, int s0, int s1, int ds, bool last) {
+      __threadfence();
+      for (int i = threadIdx.x; i < nq * (D / 4); i += kWarps * 32) {
+        const int qi = i / (D / 4), dim = 4 * (i - qi * (D / 4));
+        float M = -INFINITY, L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < n; c += kJoin) {
+          float2 e[kJoin];
+          float4 v[kJoin];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float4 v = acc[w][lane];
-      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const long long q = (long long)(a.row0 + rec.x) * a.R + qa;
-    if (F32)
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + q * D + 4 * lane) =
-          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    else
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + q * D + 4 * lane) =
-          make_uint2(pack2_bf16(o.x * inv, o.y * inv), pack2_bf16(o.z * inv, o.w * inv));
-    if (a.lse && lane == 0) a.lse[q] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          for (int x = 0; x < kJoin; ++x) {
+            const int at = min(c + x, n - 1);
+            const float* p = parts + (size_t)(at == 0 ? s0 : s1 + (at - 1) * ds) * kPart;
+            e[x] = __ldcg(reinterpret_cast<const float2*>(p) + qi);
+            v[x] = __ldcg(reinterpret_cast<const float4*>(p + 2 * kAttnQ + qi * D + dim));
+          }
+          float m = M;
+#pragma unroll
+          for (int x = 0; x < kJoin; ++x) m = fmaxf(m, e[x].x);
+          const float f0 = M == m ? 1.f : ex2_approx(M - m);
+          L *= f0;
+          o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+          M = m;
+#pragma unroll
+          for (int x = 0; x < kJoin; ++x) {
+            if (c + x < n) {
+              const float f = e[x].x == m ? 1.f : ex2_approx(e[x].x - m);
+              L += e[x].y * f;
+              o.x += v[x].x * f, o.y += v[x].y * f, o.z += v[x].z * f, o.w += v[x].w * f;
+            }
+          }
+        }
+        if (last) {
+          const long long at = (long long)crow * a.R + q0 + qi;
+          put4<F32>(a.out, at * D + dim, o, L);
+          if (a.lse && dim == 0) a.lse[at] = lse_of(M, L);
+        } else {  // in the first one's place; a thread writes the channels that it read, and the sums after all have
+          float* p = parts + (size_t)s0 * kPart;
+          *reinterpret_cast<float4*>(p + 2 * kAttnQ + qi * D + dim) = o;
+          if (dim == 0) ml[qi] = make_float2(M, L);
+        }
+      }
+      if (!last) {
+        named_bar_sync(1, kWarps * 32);
+        if ((int)threadIdx.x < nq) reinterpret_cast<float2*>(parts + (size_t)s0 * kPart)[threadIdx.x] = ml[threadIdx.x];
+      }
+    };
+    // whether this CTA is the last of n, for all threads; what they wrote before is seen by who is
+    auto leave = [&](int* counter, int n) {
+      __threadfence();
+      named_bar_sync(1, kWarps * 32);
+      if (threadIdx.x == 0) *last_flag = last_of(counter, n);
+      named_bar_sync(1, kWarps * 32);
+      return *last_flag != 0;
+    };
+    if (!leave(arrived + first, in_eight)) continue;
+    join(in_eight, first, 2 * (c_first + eight * kJoin + 1), 2, eights == 1);
+    if (eights == 1 || !leave(arrived + 2 * gridDim.x + r, eights)) continue;
+    join(eights, 2 * c_first + 1, 2 * (c_first + kJoin), 2 * kJoin, true);
   }
 }
 
@@ -822,9 +889,7 @@ int run(AttnArgs a, cudaStream_t st) {
   for (int r0 = 0; r0 < all; r0 += kAttnRows) {
     a.row0 = r0;
     a.n_rows = min(kAttnRows, all - r0);
-    int rc = launch_pdl(k, dim3(grid, chunks), kThreads, S::kBytes, st, a);
-    if (rc) return rc;
-    rc = launch_pdl(paged_combine_kernel<D, F32>, dim3(grid, a.R), 128, 0, st, a, grid, S::NQ);
+    const int rc = launch_pdl(k, dim3(grid, chunks), kThreads, S::kBytes, st, a);
     if (rc) return rc;
   }
   return KV_OK;
@@ -852,7 +917,7 @@ int launch_paged_attn(const kv_paged_shape& sh, const PageGeom& g, const SeqRows
   a.out = out;
   a.lse = lse;
   const PagedWs w = paged_ws_layout(sh);
-  a.split = reinterpret_cast<int4*>(ws + w.att_base);
+  a.arrived = reinterpret_cast<int*>(ws + w.arrived);
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.limit_ns = wait_limit_ns();
   a.kc = {0x64006400u, 0x54005400u, 0xe408e408u, 0xd480d480u};

@@ -47,9 +47,10 @@ struct RowPlan {
   int n;      // tokens to store, move or share
 };
 
-// Workspace: plans and unit prefix of the call rows, the pages taken, and the attention's partials.
+// Workspace: the attention's counters (0 between calls) and partials, plans
+// and unit prefix of the call rows, the pages taken.
 struct PagedWs {
-  size_t plan, unit, take, att_base, part, bytes;
+  size_t arrived, arrived_bytes, part, plan, unit, take, bytes;
 };
 constexpr int kUnit = 16;            // tokens per unit of the storing and moving kernels
 constexpr int kAttnRows = 1024;      // call rows per attention launch
