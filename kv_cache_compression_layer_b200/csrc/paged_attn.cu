@@ -183,6 +183,21 @@ struct Shares {
   }
 };
 
+// The last of n rows with base[row] <= at, by the whole warp: 32 probes a round. base[0] = 0 <= at.
+__device__ __forceinline__ int row_at(const int* base, int n, int at) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;  // in [lo, lo + len)
+  while (len > 1) {
+    const int step = (len + 31) >> 5;
+    const int i = lo + lane * step;
+    const bool le = lane * step < len && base[i] <= at;
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, le));
+    len = min(step, len - last * step);
+    lo += last * step;
+  }
+  return lo;
+}
+
 // The tiles [t0, t1) of a row of cost [b0, b1) that the CTA with costs [lo, hi) takes.
 struct Share {
   int tiles, t0, t1;
@@ -277,16 +292,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
   const int cta = blockIdx.x, chunk = blockIdx.y;  // the chunk of NQ query rows
   if (cta >= shares.n) return;
   const int lo = shares.lo(cta), hi = shares.lo(cta + 1);
-  int row = 0;
-  {
-    int x = 0, y = a.n_rows - 1;  // the last row with base <= lo
-    while (x < y) {
-      const int mid = (x + y + 1) >> 1;
-      if (base[mid] <= lo) x = mid;
-      else y = mid - 1;
-    }
-    row = x;
-  }
+  const int row = row_at(base, a.n_rows, lo);
   const Guard guard{abort_flag, a.c.status, a.limit_ns};
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return (bool)__all_sync(0xffffffffu, wait_bounded(bar, parity, guard));
@@ -313,76 +319,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       const int np = (lens[r] + g.P - 1) >> g.log_p;
       int win = (sh.t0 * kTile) >> g.log_p;  // lane l holds page number list[win + l]
       int entry = win + lane < np ? list[win + lane] : -1;
-      if (k >= 2) ok = wait(&q_empty[k & 1], ((k >> 1) - 1) & 1);
-      if (!ok) break;
-      // the row's queries: scaled by a power of two each, as fragments, with their sums by group and units
-      {
-        uint4* frag = reinterpret_cast<uint4*>(smem + S::kQ + (k & 1) * S::kQBytes);
-        float* meta = reinterpret_cast<float*>(smem + S::kQ + (k & 1) * S::kQBytes + S::kFrag);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int qi = nt * 8 + grp;
-          float x[W][8], top = 0.f, sum[NG];
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const long long at = ((long long)(a.row0 + r) * a.R + q0 + qi) * D + 32 * w + 8 * tig;
-            if (qi < nq) {
-              if (F32) {
-                const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
-                const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 4);
-                x[w][0] = u.x, x[w][1] = u.y, x[w][2] = u.z, x[w][3] = u.w;
-                x[w][4] = v.x, x[w][5] = v.y, x[w][6] = v.z, x[w][7] = v.w;
-              } else {
-                const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
-                x[w][0] = lo_f(u.x), x[w][1] = hi_f(u.x), x[w][2] = lo_f(u.y), x[w][3] = hi_f(u.y);
-                x[w][4] = lo_f(u.z), x[w][5] = hi_f(u.z), x[w][6] = lo_f(u.w), x[w][7] = hi_f(u.w);
-              }
-            } else {
-#pragma unroll
-              for (int n = 0; n < 8; ++n) x[w][n] = 0.f;
-            }
-          }
-#pragma unroll
-          for (int w = 0; w < W; ++w)
-#pragma unroll
-            for (int n = 0; n < 8; ++n) top = fmaxf(top, fabsf(x[w][n]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int e = max(-100, (int)(__float_as_uint(top) >> 23) - 127);  // 2^e <= top < 2^(e + 1)
-          const float up = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
-          const float down = a.scale2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
-#pragma unroll
-          for (int z = 0; z < NG; ++z) sum[z] = 0.f;
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              x[w][n] *= up;
-              sum[w * NG / W] += x[w][n];
-            }
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-              uint32_t f[4];  // a code pair holds channels n and n + 4
-#pragma unroll
-              for (int n = 0; n < 4; ++n) {
-                f[n] = pack2(x[w][n], x[w][n + 4]);
-                rest2(f[n], x[w][n], x[w][n + 4]);
-              }
-              frag[((nt * PARTS + p) * W + w) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
-            }
-          }
-#pragma unroll
-          for (int z = 0; z < NG; ++z) {
-            sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 1);
-            sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 2);
-            if (tig == 0) meta[qi * (NG + 1) + z] = sum[z];
-          }
-          if (tig == 0) meta[qi * (NG + 1) + NG] = down;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[k & 1]);
-        ++k;
-      }
       for (int t = sh.t0; t < sh.t1; ++t, ++it) {
         const int j0 = (t * kTile) >> g.log_p;
         if (j0 + ppt > win + 32) {
@@ -406,6 +342,81 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         if (++st == kStages) {
           st = 0;
           ++turn;
+        }
+        if (t > sh.t0) continue;
+        // with the row's first tile under way, its queries
+        if (k >= 2) ok = wait(&q_empty[k & 1], ((k >> 1) - 1) & 1);
+        if (!ok) {
+          ++it;  // this tile's copy is under way
+          break;
+        }
+        // scaled by a power of two each, as fragments, with their sums by group and units
+        {
+          uint4* frag = reinterpret_cast<uint4*>(smem + S::kQ + (k & 1) * S::kQBytes);
+          float* meta = reinterpret_cast<float*>(smem + S::kQ + (k & 1) * S::kQBytes + S::kFrag);
+  #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int qi = nt * 8 + grp;
+            float x[W][8], top = 0.f, sum[NG];
+  #pragma unroll
+            for (int w = 0; w < W; ++w) {
+              const long long at = ((long long)(a.row0 + r) * a.R + q0 + qi) * D + 32 * w + 8 * tig;
+              if (qi < nq) {
+                if (F32) {
+                  const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+                  const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 4);
+                  x[w][0] = u.x, x[w][1] = u.y, x[w][2] = u.z, x[w][3] = u.w;
+                  x[w][4] = v.x, x[w][5] = v.y, x[w][6] = v.z, x[w][7] = v.w;
+                } else {
+                  const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+                  x[w][0] = lo_f(u.x), x[w][1] = hi_f(u.x), x[w][2] = lo_f(u.y), x[w][3] = hi_f(u.y);
+                  x[w][4] = lo_f(u.z), x[w][5] = hi_f(u.z), x[w][6] = lo_f(u.w), x[w][7] = hi_f(u.w);
+                }
+              } else {
+  #pragma unroll
+                for (int n = 0; n < 8; ++n) x[w][n] = 0.f;
+              }
+            }
+  #pragma unroll
+            for (int w = 0; w < W; ++w)
+  #pragma unroll
+              for (int n = 0; n < 8; ++n) top = fmaxf(top, fabsf(x[w][n]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = max(-100, (int)(__float_as_uint(top) >> 23) - 127);  // 2^e <= top < 2^(e + 1)
+            const float up = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+            const float down = a.scale2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+  #pragma unroll
+            for (int z = 0; z < NG; ++z) sum[z] = 0.f;
+  #pragma unroll
+            for (int w = 0; w < W; ++w) {
+  #pragma unroll
+              for (int n = 0; n < 8; ++n) {
+                x[w][n] *= up;
+                sum[w * NG / W] += x[w][n];
+              }
+  #pragma unroll
+              for (int p = 0; p < PARTS; ++p) {
+                uint32_t f[4];  // a code pair holds channels n and n + 4
+  #pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                  f[n] = pack2(x[w][n], x[w][n + 4]);
+                  rest2(f[n], x[w][n], x[w][n + 4]);
+                }
+                frag[((nt * PARTS + p) * W + w) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+              }
+            }
+  #pragma unroll
+            for (int z = 0; z < NG; ++z) {
+              sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 1);
+              sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 2);
+              if (tig == 0) meta[qi * (NG + 1) + z] = sum[z];
+            }
+            if (tig == 0) meta[qi * (NG + 1) + NG] = down;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full[k & 1]);
+          ++k;
         }
       }
     }
