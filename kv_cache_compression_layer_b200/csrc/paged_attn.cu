@@ -28,13 +28,13 @@
 // codes, free of bank conflicts by the page's order of words and the order in
 // which a tile's keys take the rows.
 //
-// Work. Rows are cut into tiles of 64 tokens; a row costs its tiles plus a
+// Work. Rows are cut into tiles of 128 tokens; a row costs its tiles plus a
 // charge for starting and leaving it (an empty row 1). The CTAs (up to three
 // per SM) take equal shares of the total, contiguous over rows. In a CTA one
 // warp runs ahead, over row ends too: it streams the tiles into a ring of stages
 // with bulk copies (the four parts of a page's 64 tokens are each contiguous)
 // and lays out each row's queries as matrix fragments. Four warps take 16
-// tokens of a tile each, with a softmax of their own that is joined when the
+// times two tokens of a tile each, with a softmax of their own that is joined when the
 // CTA leaves the row. CTAs that share a row leave partials: of each eight in
 // turn the one that comes last, by a counter, joins them, and of those the last
 // joins the eights (one CTA loads a partial in no less than 0.04 us, and eight
@@ -48,11 +48,11 @@
 namespace kvc {
 namespace {
 
-constexpr int kTile = 64;     // tokens per tile
+constexpr int kTile = 128;    // tokens per tile: two times 16 for each of the warps that attend
 constexpr int kWarps = 4;     // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kRowCost = 4;   // of starting and leaving a row, in tiles
-constexpr int kMinShare = 4;  // cost of a CTA's share, at least
+constexpr int kRowCost = 2;   // of starting and leaving a row, in tiles
+constexpr int kMinShare = 3;  // cost of a CTA's share, at least
 constexpr int kJoin = 8;      // partials joined at once
 constexpr float kGrow = 8.f;  // the running maximum moves when a logit passes it by this (log2 units)
 
@@ -61,7 +61,7 @@ constexpr float kGrow = 8.f;  // the running maximum moves when a logit passes i
 // queries (matrix fragments; per query its sums by group and its unit).
 template <int D, int NG, int NT, bool F32>
 struct Smem {
-  static constexpr int kStages = NG == 4 ? 4 : 5;
+  static constexpr int kStages = 2;
   static constexpr int kCode = kTile * D / 2, kScale = kTile * NG * 4;
   static constexpr int kV = kCode, kKs = 2 * kCode, kVs = kKs + kScale, kStage = kVs + kScale;
   static constexpr int NQ = NT * 8, kORow = D + 4;
@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
   const int row = row_at(base, a.n_rows, lo);
   const Guard guard{abort_flag, a.c.status, a.limit_ns};
   auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
     return (bool)__all_sync(0xffffffffu, wait_bounded(bar, parity, guard));
   };
   const int grp = lane >> 2, tig = lane & 3;
@@ -522,21 +523,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     }
     float om = 1.f, s_top = -1.f;  // scale of p', and the largest step that it is made for
 
-    // 16 keys from each of U stages, of tiles t and after; MASKED (U = 1): some are hidden from some query.
-    auto attend = [&](auto uu, const uint8_t* st0, const uint8_t* st1, int t) {
+    // The warp's 16 keys of each of the halves u0 .. u0 + U - 1 of tile t in stage st; MASKED (U = 1): some are hidden
+    // from some query.
+    auto attend = [&](auto uu, const uint8_t* st, int u0, int t) {
       constexpr int U = decltype(uu)::value;
       constexpr bool MASKED = U == 1;
-      const uint8_t* sts[2] = {st0, st1};
-      const int key0 = t * kTile + krow;  // of matrix row grp; row grp + 8 is 8 further
+      const int row0 = krow + 64 * u0;          // token of the tile in matrix row grp; row grp + 8 is 8 further
+      const int key0 = t * kTile + row0;
       // ---- logits: rows keys, columns queries
       float y[U][NT][4];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const uint8_t* st = sts[u];
         uint32_t kw[2][W], ks[2][NG];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const uint8_t* kp = st + (krow + 8 * x) * (D / 2) + tig * (D / 8);
+          const uint8_t* kp = st + (row0 + 64 * u + 8 * x) * (D / 2) + tig * (D / 8);
           if constexpr (W == 4) {
             const uint4 v = *reinterpret_cast<const uint4*>(kp);
             kw[x][0] = v.x, kw[x][1] = v.y, kw[x][2] = v.z, kw[x][3] = v.w;
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
             const uint2 v = *reinterpret_cast<const uint2*>(kp);
             kw[x][0] = v.x, kw[x][1] = v.y;
           }
-          load_scales<NG>(st + S::kKs + (krow + 8 * x) * (NG * 4), ks[x]);
+          load_scales<NG>(st + S::kKs + (row0 + 64 * u + 8 * x) * (NG * 4), ks[x]);
         }
         float acc[NT][NG][4];
 #pragma unroll
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          load_scales<NG>(sts[u] + S::kVs + (krow + 8 * x) * (NG * 4), vs[u][x]);
+          load_scales<NG>(st + S::kVs + (row0 + 64 * u + 8 * x) * (NG * 4), vs[u][x]);
           if constexpr (MASKED) {
             if (key0 + 8 * x >= len) {
 #pragma unroll
@@ -652,7 +653,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const uint8_t* st = sts[u];
         uint32_t b[NT][NG][PARTS][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         uint32_t vw[4][(W + 1) / 2];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int vr = ((x & 1) ? vrow2 : vrow) + (x >> 1) * 8;
+          const int vr = ((x & 1) ? vrow2 : vrow) + (x >> 1) * 8 + 64 * (u0 + u);
           const uint8_t* vp = st + S::kV + vr * (D / 2) + vplace * (D / 16);
           if constexpr (W == 4) {
             const uint2 v = *reinterpret_cast<const uint2*>(vp);
@@ -723,28 +723,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       }
     };
 
-    for (int t = sh.t0; ok && t < sh.t1;) {
-      // two tiles at once while every query sees all of them
-      const bool two = t + 2 <= sh.t1 && (t + 1) * kTile + warp * 16 + 16 <= lim_min;
-      const int s0 = st, s1 = st + 1 == kStages ? 0 : st + 1;
-      ok = wait(&full[s0], turn & 1);
-      if (two && ok) ok = wait(&full[s1], (turn + (s1 == 0)) & 1);
+    for (int t = sh.t0; t < sh.t1; ++t) {
+      ok = wait(&full[st], turn & 1);
       if (!ok) break;
-      const uint8_t *st0 = smem + s0 * S::kStage, *st1 = smem + s1 * S::kStage;
-      if (two)
-        attend(std::integral_constant<int, 2>{}, st0, st1, t);
-      else if (t * kTile + warp * 16 < len)
-        attend(std::integral_constant<int, 1>{}, st0, st1, t);
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&empty[s0]);
-        if (two) mbar_arrive(&empty[s1]);
+      const uint8_t* stage = smem + st * S::kStage;
+      const int tok = t * kTile + warp * 16;
+      if (tok + 64 + 16 <= lim_min) {  // every query sees all of them
+        attend(std::integral_constant<int, 2>{}, stage, 0, t);
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < 2 && tok + 64 * u < len; ++u) attend(std::integral_constant<int, 1>{}, stage, u, t);
       }
-      const int n = two ? 2 : 1;
-      t += n;
-      st += n;
-      if (st >= kStages) {
-        st -= kStages;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      if (++st == kStages) {
+        st = 0;
         ++turn;
       }
     }
