@@ -3,7 +3,9 @@
 ``Compressor`` owns the device memory (allocated through torch, the only use
 of torch here besides streams) and calls the C-ABI entry points in the
 path's order: allocate -> score -> SSS -> select + gather -> decode init,
-then one ``kv_decode_attn_update`` per decode step.
+then one ``kv_decode_attn_update`` per decode step. ``compress_paged`` ends in
+the pages of a ``PagedCache`` instead: the kept tokens are quantised to 4 bits
+straight from K and V.
 """
 from __future__ import annotations
 
@@ -12,8 +14,9 @@ from typing import Optional, Sequence
 import torch
 
 from . import (KV_BF16, META_INTS, kv_allocate, kv_decode_attn_update, kv_decode_init, kv_decode_scratch_bytes,
-               kv_params, kv_score, kv_select_gather, kv_shape, kv_sss, kv_total_slots, kv_workspace_bytes,
+               kv_params, kv_score, kv_select, kv_select_gather, kv_shape, kv_sss, kv_total_slots, kv_workspace_bytes,
                make_cache)
+from .paged import PagedCache
 
 
 def torch_dtype(dtype_code: int):
@@ -31,6 +34,7 @@ class Compressor:
         self.R = shape.group * shape.w
         self.L_rows = [l for l in self.L for _ in range(nl * H)]
         self.n_keys = sum(self.L_rows)
+        self.key_off = torch.tensor([0] + self.L_rows[:-1], dtype=torch.int64).cumsum(0).to(self.device)
         self.n_slots = kv_total_slots(shape, self.L, params)
         if self.n_slots < 0:
             raise ValueError("invalid shape or parameters")
@@ -81,6 +85,26 @@ class Compressor:
         self.sss(stream)
         self.select_gather(K, V, stream)
         self.decode_init(stream)
+
+    def compress_paged(self, cache: PagedCache, seqs: Sequence[int], qwin, K, V, S,
+                       spikes: Optional[torch.Tensor] = None, stream=None):
+        """allocate -> score -> (harness spikes) -> SSS -> select, then the kept tokens of the batch's
+        sequence i, quantised, behind those of sequence seqs[i] of ``cache`` (kv_paged_append; no
+        compacted copy is written, and the decode cache of this object is not touched but for
+        ``pos``, which holds the kept positions)."""
+        sh, cs = self.shape, cache.shape
+        if (cs.n_layers, cs.n_kv_heads, cs.head_dim, cs.dtype) != (sh.n_layers, sh.n_kv_heads, sh.head_dim, sh.dtype):
+            raise ValueError("the cache holds rows of another shape")
+        if len(seqs) != len(self.L):
+            raise ValueError(f"{len(self.L)} sequences, got {len(seqs)}")
+        self.allocate(S, stream)
+        self.score(qwin, K, stream)
+        if spikes is not None:
+            self.s.mul_(spikes)
+        self.sss(stream)
+        kv_select(self.shape, self.L, self.s_hat, self.b, self.slot_off, self.pos, stream)
+        cache.append(seqs, K, V, count=self.b, src_off=self.key_off, idx=self.pos, idx_off=self.slot_off,
+                     stream=stream)
 
     def compress_from_host(self, host: dict, dev: dict, stream=None, copy_stream=None) -> int:
         """The same path with its inputs in pinned host memory, the copies overlapped with the work.
