@@ -53,9 +53,13 @@ int make_row_map(const kv_shape& sh, const int32_t* L, int32_t n_seq, RowMap& m)
 int64_t total_keys(const RowMap& m) { return m.key_off[m.n_seq]; }
 
 int sm_count() {
+  static std::atomic<int> known[64];  // by device; a device's count does not change
   int dev = 0, n = 0;
-  cudaGetDevice(&dev);
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0)
+    return n;
+  n = 0;
   cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (n > 0 && dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n > 0 ? n : 1;
 }
 

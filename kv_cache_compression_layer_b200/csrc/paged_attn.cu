@@ -41,6 +41,7 @@
 // of them in one latency). Every sum has a fixed order.
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "paged_common.cuh"
@@ -884,8 +885,15 @@ template <int D, int NG, int NT, bool F32>
 int run(AttnArgs a, cudaStream_t st) {
   using S = Smem<D, NG, NT, F32>;
   auto k = paged_attn_kernel<D, NG, NT, F32>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
-    return KV_ERR_CUDA;
+  static std::atomic<unsigned long long> ready{0};  // devices on which the kernel may take its shared memory
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KV_ERR_CUDA;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
+      return KV_ERR_CUDA;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   const int chunks = (a.R + S::NQ - 1) / S::NQ;
   const int per_sm = NT == 1 && !F32 ? kAttnCtasPerSm : 2;
   const int grid = max(1, sm_count() * per_sm / chunks);
