@@ -53,7 +53,7 @@ constexpr int kTile = 128;    // tokens per tile: two times 16 for each of the w
 constexpr int kWarps = 4;     // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kRowCost = 2;   // of starting and leaving a row, in tiles
-constexpr int kMinShare = 3;  // cost of a CTA's share, at least
+constexpr int kMinShare = 2;  // cost of a CTA's share, at least
 constexpr int kJoin = 8;      // partials joined at once
 constexpr float kGrow = 8.f;  // the running maximum moves when a logit passes it by this (log2 units)
 
@@ -805,45 +805,57 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     }
     // a shared row: joins n partials, the first at slot s0 and the others at slots s1, s1 + ds, ..
     auto join = [&](int n, int s0, int s1, int ds, bool last) {
-      __threadfence();
-      for (int i = threadIdx.x; i < nq * (D / 4); i += kWarps * 32) {
-        const int qi = i / (D / 4), dim = 4 * (i - qi * (D / 4));
-        float M = -INFINITY, L = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int items = nq * (D / 4);
+      for (int i0 = threadIdx.x; i0 < items; i0 += 2 * kWarps * 32) {  // two items' loads at once
+        float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
+        float4 o[2];
+        o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int qi[2] = {i0 / (D / 4), min(i0 + kWarps * 32, items - 1) / (D / 4)};
+        const int dim = 4 * (i0 % (D / 4));  // of both: the threads are a multiple of D / 4
         for (int c = 0; c < n; c += kJoin) {
-          float2 e[kJoin];
-          float4 v[kJoin];
+          float2 e[2][kJoin];
+          float4 v[2][kJoin];
 #pragma unroll
           for (int x = 0; x < kJoin; ++x) {
             const int at = min(c + x, n - 1);
             const float* p = parts + (size_t)(at == 0 ? s0 : s1 + (at - 1) * ds) * kPart;
-            e[x] = __ldcg(reinterpret_cast<const float2*>(p) + qi);
-            v[x] = __ldcg(reinterpret_cast<const float4*>(p + 2 * kAttnQ + qi * D + dim));
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              e[y][x] = __ldcg(reinterpret_cast<const float2*>(p) + qi[y]);
+              v[y][x] = __ldcg(reinterpret_cast<const float4*>(p + 2 * kAttnQ + qi[y] * D + dim));
+            }
           }
-          float m = M;
 #pragma unroll
-          for (int x = 0; x < kJoin; ++x) m = fmaxf(m, e[x].x);
-          const float f0 = M == m ? 1.f : ex2_approx(M - m);
-          L *= f0;
-          o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
-          M = m;
+          for (int y = 0; y < 2; ++y) {
+            float m = M[y];
 #pragma unroll
-          for (int x = 0; x < kJoin; ++x) {
-            if (c + x < n) {
-              const float f = e[x].x == m ? 1.f : ex2_approx(e[x].x - m);
-              L += e[x].y * f;
-              o.x += v[x].x * f, o.y += v[x].y * f, o.z += v[x].z * f, o.w += v[x].w * f;
+            for (int x = 0; x < kJoin; ++x) m = fmaxf(m, e[y][x].x);
+            const float f0 = M[y] == m ? 1.f : ex2_approx(M[y] - m);
+            L[y] *= f0;
+            o[y].x *= f0, o[y].y *= f0, o[y].z *= f0, o[y].w *= f0;
+            M[y] = m;
+#pragma unroll
+            for (int x = 0; x < kJoin; ++x) {
+              if (c + x < n) {
+                const float f = e[y][x].x == m ? 1.f : ex2_approx(e[y][x].x - m);
+                L[y] += e[y][x].y * f;
+                o[y].x += v[y][x].x * f, o[y].y += v[y][x].y * f;
+                o[y].z += v[y][x].z * f, o[y].w += v[y][x].w * f;
+              }
             }
           }
         }
-        if (last) {
-          const long long at = (long long)crow * a.R + q0 + qi;
-          put4<F32>(a.out, at * D + dim, o, L);
-          if (a.lse && dim == 0) a.lse[at] = lse_of(M, L);
-        } else {  // in the first one's place; a thread writes the channels that it read, and the sums after all have
-          float* p = parts + (size_t)s0 * kPart;
-          *reinterpret_cast<float4*>(p + 2 * kAttnQ + qi * D + dim) = o;
-          if (dim == 0) ml[qi] = make_float2(M, L);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          if (y == 1 && i0 + kWarps * 32 >= items) continue;
+          if (last) {
+            const long long at = (long long)crow * a.R + q0 + qi[y];
+            put4<F32>(a.out, at * D + dim, o[y], L[y]);
+            if (a.lse && dim == 0) a.lse[at] = lse_of(M[y], L[y]);
+          } else {  // in the first one's place; a thread writes the channels that it read, the sums follow
+            *reinterpret_cast<float4*>(parts + (size_t)s0 * kPart + 2 * kAttnQ + qi[y] * D + dim) = o[y];
+            if (dim == 0) ml[qi[y]] = make_float2(M[y], L[y]);
+          }
         }
       }
       if (!last) {
@@ -853,9 +865,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     };
     // whether this CTA is the last of n, for all threads; what they wrote before is seen by who is
     auto leave = [&](int* counter, int n) {
-      __threadfence();
       named_bar_sync(1, kWarps * 32);
-      if (threadIdx.x == 0) *last_flag = last_of(counter, n);
+      if (threadIdx.x == 0) {
+        __threadfence();  // what the barrier ordered before it is seen before the count
+        *last_flag = last_of(counter, n);
+        __threadfence();
+      }
       named_bar_sync(1, kWarps * 32);
       return *last_flag != 0;
     };
