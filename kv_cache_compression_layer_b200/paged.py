@@ -35,7 +35,9 @@ class PagedCache:
         if device is None:
             device = table.device if table is not None else "cuda"
         device = torch.device(device)
-        if device.type == "cuda" and device.index is None:
+        if device.type != "cuda":
+            raise ValueError("the page lists are on a CUDA device (pages alone may be pinned host memory)")
+        if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
         self.device = device
         page_bytes = kv_paged_page_bytes(shape)
@@ -84,6 +86,8 @@ class PagedCache:
 
     def _call_rows(self, seqs: Sequence[int], layers: Optional[Tuple[int, int]]) -> Tuple[int, int, int]:
         l0, nl = (0, self.shape.n_layers) if layers is None else layers
+        if l0 < 0 or nl < 1 or l0 + nl > self.shape.n_layers:
+            raise ValueError(f"layers: (first, number) within {self.shape.n_layers}")
         if self.on_host:
             raise ValueError("the pages are on the host: copy the sequences to a cache on a device")
         if not 0 < len(seqs) <= KV_MAX_SEQ:
@@ -125,7 +129,7 @@ class PagedCache:
                     raise ValueError("idx goes with idx_off")
                 self._is("idx", idx, torch.int32, idx.numel())
                 self._is("idx_off", idx_off, torch.int64, n, at_least=True)
-        if n_src == 0:
+        if count is None and n_src == 0:
             return
         with self._here():
             kv_paged_append(self.shape, self.cache, seqs, K, V, n_src, n_each, count, src_off, idx, idx_off, l0, nl,

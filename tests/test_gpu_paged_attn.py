@@ -189,3 +189,100 @@ def test_bad_page_numbers_are_reported():
     out = cache.attend([0, 1], q)
     assert cache.read_status() == kv.KV_DEV_BOUNDS
     m.check_attention(q, out, None, [0, 1], 1, rows_at={1})
+
+
+def test_pages_beyond_four_gigabytes():
+    """Pages whose byte offset passes 32 bits are written, read, attended over and copied."""
+    rng = np.random.default_rng(14)
+    n_pages, low = 480_000, 470_000  # 9216 bytes a page: the free ones start at 4.3e9
+    sh = kv.make_paged_shape(3, 1, 1, 4, 128, kv.KV_BF16, n_pages, low, 64, 64)
+    table = torch.zeros(3, low, dtype=torch.int32, device="cuda")
+    table[0] = torch.arange(low, device="cuda")
+    lens = torch.tensor([low * 64, 0, 0], dtype=torch.int32, device="cuda")
+    cache = kv.PagedCache(sh, table=table, lens=lens)
+    m = pg.Model(sh)
+    m.ref[:low] = 1
+    m.lists[0], m.len[0] = [-1], low * 64  # held, and not looked at
+    K, V = pg.tokens(rng, 300, 128, 1)
+    m.append([1], [K], [V])
+    assert m.lists[1] == list(range(low, low + 5)) and low * 9216 > 1 << 32
+    cache.append([1], pg.up(K, 1, cache.device), pg.up(V, 1, cache.device))
+    cache.copy_to(cache, [1], [2])
+    m.copy_to(m, [1], [2])
+    m.check_values(cache, [1, 2])
+    attend(cache, m, rng, [2, 1])
+    assert cache.table[1, :5].tolist() == m.lists[1] and cache.table[2, :5].tolist() == m.lists[2]
+
+
+def test_two_calls_at_once():
+    """Two attentions over one pool on two streams, each with a workspace of its own, many times."""
+    rng = np.random.default_rng(15)
+    cache, m = pg.make(n_seqs=4, n_layers=2, heads=2, group=4, page=16, max_pages=60)
+    pg.fill(cache, m, rng.integers(1, 900, m.rows), rng)
+    ws = torch.zeros_like(cache.ws)
+    second = kv.make_paged_cache(cache.pages, cache.table, cache.lens, cache.ref, cache.free_bits, cache.status, ws)
+    q = [queries(rng, m, m.call_rows(s), 4, 1, cache.device) for s in ([0, 1], [1, 2, 3])]
+    want = [cache.attend(s, x) for s, x in zip(([0, 1], [1, 2, 3]), q)]
+    outs = [[torch.empty_like(x) for _ in range(20)] for x in q]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        kv.kv_paged_attn(cache.shape, cache.cache, [0, 1], q[0], outs[0][i], stream=streams[0])
+        kv.kv_paged_attn(cache.shape, second, [1, 2, 3], q[1], outs[1][i], stream=streams[1])
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
+
+
+def test_a_branch_in_a_graph():
+    """Fork, append, attention and free captured once and replayed: every replay gives the same, and leaves the cache
+    as it was."""
+    rng = np.random.default_rng(16)
+    cache, m = pg.make(n_seqs=3, n_layers=2, heads=2, group=2, d=64, qg=32, page=16, max_pages=10)
+    counts = np.zeros(m.rows, int)
+    counts[: m.rps] = [0, 16, 33, 150]
+    pg.fill(cache, m, counts, rng)
+    dev = cache.device
+    K, V = pg.tokens(rng, 2 * m.rps, 64, 1)
+    k, v = pg.up(K, 1, dev), pg.up(V, 1, dev)
+    m.fork([0, 0], [1, 2])
+    m.append(m.call_rows([1, 2]), K[:, None], V[:, None])
+    q = queries(rng, m, m.call_rows([1, 2]), 2, 1, dev)
+    out = torch.empty_like(q)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        cache.fork([0, 0], [1, 2])
+        cache.append([1, 2], k, v)
+        cache.attend([1, 2], q, out)
+        cache.free([1, 2])
+    lists = [list(x) for x in m.lists]
+    for _ in range(3):
+        out.fill_(5)
+        graph.replay()
+        torch.cuda.synchronize()
+        m.check_attention(q, out, None, [1, 2], 1)
+        table = cache.table.cpu().numpy()
+        for r in m.call_rows([1, 2]):  # what is behind a row's list stays
+            assert table[r, : len(lists[r])].tolist() == lists[r]
+    m.free([1, 2])
+    m.check(cache)
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-6, 1e4, 1e30])
+def test_values_of_any_size(scale):
+    """Steps of V far from 1, and rows in which they grow and shrink by powers of ten."""
+    rng = np.random.default_rng(17)
+    cache, m = pg.make(n_seqs=1, n_layers=1, heads=2, group=3, qg=32, max_pages=8)
+    n = 300
+    K, V = pg.tokens(rng, 2 * n, 128, 1)
+    V = pg.bf16(V * scale)
+    V[n:] = pg.bf16(V[n:] * np.repeat(10.0 ** rng.integers(-3, 4, n // 10), 10)[:, None])
+    V[:40] = 0.0  # steps of 0 first
+    m.append([0, 1], K.reshape(2, n, 128), V.reshape(2, n, 128))
+    cache.append([0], pg.up(K, 1, cache.device), pg.up(V, 1, cache.device))
+    q = queries(rng, m, [0, 1], 3, 1, cache.device)
+    out = torch.empty_like(q)
+    cache.attend([0], q, out)
+    m.check_attention(q, out, None, [0], 1)

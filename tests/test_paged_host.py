@@ -161,6 +161,10 @@ def test_wrapper_refuses_what_does_not_match():
            lambda: c.attend([0], x), lambda: c.attend([0], torch.zeros(n, 8, d)),
            lambda: c.attend([0], torch.zeros(n, 8, d, dtype=torch.bfloat16), lse=torch.zeros(n, 7)),
            lambda: c.attend([0], torch.zeros(n, 8, d, dtype=torch.bfloat16), out=x),
+           lambda: c.append([0], x, x, layers=(0, 0)), lambda: c.attend([0], x, layers=(1, 3)),
+           lambda: c.load([0], x, x, off, layers=(-1, 2)),
+           lambda: kv.PagedCache(shape(), device="cpu"), lambda: kv.PagedCache(shape(quant_group=16), device="cuda:0"),
+           lambda: kv.PagedCache(shape(), table=cnt, lens=cnt),
            lambda: c.compact([0], [1], cnt, off, cnt.long()), lambda: c.compact([0], [1], cnt.long(), off, cnt)]
     for f in bad:
         with pytest.raises(ValueError):
