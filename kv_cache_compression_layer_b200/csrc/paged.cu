@@ -410,8 +410,8 @@ struct Row16;
 template <>
 struct Row16<false> {
   uint4 a, b;
-  __device__ __forceinline__ void load(const void* base, long long row, int d, int l) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + row * d) + 2 * l;
+  __device__ __forceinline__ void load(const void* base, long long off) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + off);
     a = p[0];
     b = p[1];
   }
@@ -438,8 +438,8 @@ struct Row16<false> {
 template <>
 struct Row16<true> {
   float4 v[4];
-  __device__ __forceinline__ void load(const void* base, long long row, int d, int l) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + row * d) + 4 * l;
+  __device__ __forceinline__ void load(const void* base, long long off) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = p[i];
   }
@@ -550,30 +550,38 @@ __global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 3) paged_store_kern
   const int u0 = (int)(w * total / nw), u1 = (int)((w + 1) * total / nw);
   if (u0 >= u1) return;
   uint8_t* st = stage[warp];
-  int row = find_unit_row(a.unit, n_rows, u0);
   int bad = 0;
+  // the row of the next unit: its units [row_u0, row_u1), plan and source
+  int row = -1, row_u0 = 0, row_u1 = -1;
+  RowPlan p{};
+  long long base = 0, at = 0;
 
-  // A unit: where it goes (page, place of its first token, its new tokens [f, e)) and, in lane t, the source row of
-  // its token t (-1: none).
+  // A unit: where it goes (page, place of its first token, its new tokens [f, e)) and, in lane t, the element offset of
+  // the source row of its token t (-1: none).
   struct Unit {
     int page, place, f, e;
     long long src;
   };
   auto unit_at = [&](int u) {
     Unit x;
-    if (u >= a.unit[row + 1]) row = find_unit_row(a.unit, n_rows, u);
-    const RowPlan p = a.plan[row];
-    const int trow = table_row(a.rows, row);
-    const int pos0 = (p.old / kUnit + u - a.unit[row]) * kUnit;
+    if (u >= row_u1) {
+      row = find_unit_row(a.unit, n_rows, u);
+      row_u0 = a.unit[row];
+      row_u1 = a.unit[row + 1];
+      p = a.plan[row];
+      base = a.src_off ? a.src_off[row] : (long long)row * a.n_each;
+      if (a.idx) at = a.idx_off[row];
+    }
+    const int pos0 = (p.old / kUnit + u - row_u0) * kUnit;
     x.f = max(p.old - pos0, 0);
     x.e = min(kUnit, p.old + p.n - pos0);
     const int j = pos0 >> g.log_p;
     x.place = pos0 & (g.P - 1);
     if (j >= p.fresh) {
       x.page = a.take[p.take + j - p.fresh];
-      if (x.place == 0 && lane == 0) claim_page(a.c, g, trow, j, x.page);
+      if (x.place == 0 && lane == 0) claim_page(a.c, g, table_row(a.rows, row), j, x.page);
     } else {
-      x.page = a.c.table[(size_t)trow * g.max_pages + j];
+      x.page = a.c.table[(size_t)table_row(a.rows, row) * g.max_pages + j];
       if (x.page < 0 || x.page >= g.n_pages) {
         bad |= KV_DEV_BOUNDS;
         x.f = x.e = 0;  // nothing of it is stored
@@ -583,32 +591,32 @@ __global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 3) paged_store_kern
     x.src = -1;
     if (lane >= x.f && lane < x.e) {
       const int t = pos0 + lane - p.old;
-      const long long base = a.src_off ? a.src_off[row] : (long long)row * a.n_each;
-      x.src = base + (a.idx ? (long long)a.idx[a.idx_off[row] + t] : (long long)t);
-      if (x.src < 0 || x.src >= a.n_src) {
-        x.src = -1;
-        bad |= KV_DEV_RANGE;
-      }
+      const long long src = base + (a.idx ? (long long)a.idx[at + t] : (long long)t);
+      if (src < 0 || src >= a.n_src) bad |= KV_DEV_RANGE;
+      else x.src = src * D;
     }
     return x;
   };
-  Row16<F32> cur[ITER];
-  auto load = [&](Row16<F32>(&r)[ITER], const void* from, long long src) {
-#pragma unroll
-    for (int it = 0; it < ITER; ++it) {
-      const long long s = __shfl_sync(0xffffffffu, src, it * TPI + sub);
-      if (s >= 0) r[it].load(from, s, D, l);
-      else r[it].zero();
-    }
-  };
 
-  Unit now = unit_at(u0);
+  Unit now{};
+  long long off[ITER];  // of this lane's tokens' channels
 #pragma unroll 1
   for (int i = 2 * u0; i < 2 * u1; ++i) {
     const bool v = i & 1;  // the unit's V, else its K
-    if (!v && i > 2 * u0) now = unit_at(i >> 1);
-    const Unit here = now;
-    load(cur, v ? a.V : a.K, now.src);
+    if (!v) {
+      now = unit_at(i >> 1);
+#pragma unroll
+      for (int it = 0; it < ITER; ++it) {
+        const long long s = __shfl_sync(0xffffffffu, now.src, it * TPI + sub);
+        off[it] = s < 0 ? -1 : s + 16 * l;
+      }
+    }
+    Row16<F32> cur[ITER];
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+      if (off[it] >= 0) cur[it].load(v ? a.V : a.K, off[it]);
+      else cur[it].zero();
+    }
     __syncwarp();  // the previous part has left the stage
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
@@ -620,8 +628,8 @@ __global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 3) paged_store_kern
         sk[0] = z.w[0];
         sk[W] = z.w[1];
       } else {  // 16-bit words (p, h), p = channel % 32 / 4, in places swapped by the token's bit 1
-        const int p = (4 * (l & 1)) ^ ((t & 2) << 1);
-        uint16_t* sv = reinterpret_cast<uint16_t*>(st) + t * (D / 4) + p * W + (l >> 1);
+        const int pv = (4 * (l & 1)) ^ ((t & 2) << 1);
+        uint16_t* sv = reinterpret_cast<uint16_t*>(st) + t * (D / 4) + pv * W + (l >> 1);
         sv[0] = (uint16_t)z.w[0];
         sv[W] = (uint16_t)(z.w[0] >> 16);
         sv[2 * W] = (uint16_t)z.w[1];
@@ -630,14 +638,18 @@ __global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 3) paged_store_kern
       if (l % LG == 0) reinterpret_cast<uint32_t*>(st + kCode)[t * G + l / LG] = z.scale;
     }
     __syncwarp();
-    uint8_t* pg = a.c.pages + (size_t)here.page * g.bytes;
+    uint8_t* pg = a.c.pages + (size_t)now.page * g.bytes;
     constexpr int RC = D / 2 / 16;  // 16-byte pieces of a token's codes
     const uint4* ss = reinterpret_cast<const uint4*>(st);
-    uint4* d = reinterpret_cast<uint4*>(pg + (v ? g.v : 0) + here.place * (D / 2));
-    for (int x = here.f * RC + lane; x < here.e * RC; x += 32) d[x] = ss[x];
+    uint4* d = reinterpret_cast<uint4*>(pg + (v ? g.v : 0) + now.place * (D / 2));
     const uint32_t* sx = reinterpret_cast<const uint32_t*>(st + kCode);
-    uint32_t* dx = reinterpret_cast<uint32_t*>(pg + (v ? g.vs : g.ks)) + here.place * G;
-    for (int x = here.f * G + lane; x < here.e * G; x += 32) dx[x] = sx[x];
+    uint32_t* dx = reinterpret_cast<uint32_t*>(pg + (v ? g.vs : g.ks)) + now.place * G;
+#pragma unroll
+    for (int x = lane; x < kUnit * RC; x += 32)
+      if (x >= now.f * RC && x < now.e * RC) d[x] = ss[x];
+#pragma unroll
+    for (int x = lane; x < (kUnit * G + 31) / 32 * 32; x += 32)
+      if (x >= now.f * G && x < now.e * G) dx[x] = sx[x];
   }
   if (bad) atomicOr(a.c.status, bad);
 }
