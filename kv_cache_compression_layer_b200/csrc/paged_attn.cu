@@ -62,7 +62,7 @@ constexpr float kGrow = 8.f;  // the running maximum moves when a logit passes i
 // queries (matrix fragments; per query its sums by group and its unit).
 template <int D, int NG, int NT, bool F32>
 struct Smem {
-  static constexpr int kStages = 2;
+  static constexpr int kStages = D == 64 ? 4 : 2;  // as many as leave room for three CTAs an SM
   static constexpr int kCode = kTile * D / 2, kScale = kTile * NG * 4;
   static constexpr int kV = kCode, kKs = 2 * kCode, kVs = kKs + kScale, kStage = kVs + kScale;
   static constexpr int NQ = NT * 8, kORow = D + 4;
