@@ -524,11 +524,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     }
     float om = 1.f, s_top = -1.f;  // scale of p', and the largest step that it is made for
 
-    // The warp's 16 keys of each of the halves u0 .. u0 + U - 1 of tile t in stage st; MASKED (U = 1): some are hidden
-    // from some query.
-    auto attend = [&](auto uu, const uint8_t* st, int u0, int t) {
+    // The warp's 16 keys of each of the halves u0 .. u0 + U - 1 of tile t in stage st; MASKED: some are hidden from
+    // some query.
+    auto attend = [&](auto uu, auto mk, const uint8_t* st, int u0, int t) {
       constexpr int U = decltype(uu)::value;
-      constexpr bool MASKED = U == 1;
+      constexpr bool MASKED = decltype(mk)::value;
       const int row0 = krow + 64 * u0;          // token of the tile in matrix row grp; row grp + 8 is 8 further
       const int key0 = t * kTile + row0;
       // ---- logits: rows keys, columns queries
@@ -729,11 +729,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       if (!ok) break;
       const uint8_t* stage = smem + st * S::kStage;
       const int tok = t * kTile + warp * 16;
-      if (tok + 64 + 16 <= lim_min) {  // every query sees all of them
-        attend(std::integral_constant<int, 2>{}, stage, 0, t);
+      // both halves at once where every query sees all of them and the registers allow (16 queries spill: 192 rows of
+      // 6400 keys, g = 16, 102 us against 81)
+      constexpr int U = NT == 1 ? 2 : 1;
+      if (tok + 64 + 16 <= lim_min) {
+#pragma unroll 1
+        for (int u = 0; u < 2; u += U)
+          attend(std::integral_constant<int, U>{}, std::false_type{}, stage, u, t);
       } else {
 #pragma unroll 1
-        for (int u = 0; u < 2 && tok + 64 * u < len; ++u) attend(std::integral_constant<int, 1>{}, stage, u, t);
+        for (int u = 0; u < 2 && tok + 64 * u < len; ++u)
+          attend(std::integral_constant<int, 1>{}, std::true_type{}, stage, u, t);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
