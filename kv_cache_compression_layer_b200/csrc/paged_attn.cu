@@ -729,9 +729,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       if (!ok) break;
       const uint8_t* stage = smem + st * S::kStage;
       const int tok = t * kTile + warp * 16;
-      // both halves at once where every query sees all of them and the registers allow (16 queries spill: 192 rows of
-      // 6400 keys, g = 16, 102 us against 81)
-      constexpr int U = NT == 1 ? 2 : 1;
+      // both halves at once where every query sees all of them and the registers allow (16 queries spill, 192 rows of
+      // 6400 keys, g = 16, 102 us against 81; 8 queries with groups of 32, 62.3 against 60.9)
+      constexpr int U = NT == 1 && (NG < 4 || F32) ? 2 : 1;
       if (tok + 64 + 16 <= lim_min) {
 #pragma unroll 1
         for (int u = 0; u < 2; u += U)
