@@ -8,7 +8,8 @@
 // data kernel moves the tokens and, where it reaches the first token of a new
 // page, enters the page into the row's list, its count and the bitmap. No
 // device wait, no atomics whose order shows: a page's count is an integer sum
-// and the bitmap a set.
+// and the bitmap a set. The plan is a chain of dependent loads and block sums
+// of one CTA, 5 to 10 us; the other kernels are bound by the bytes they move.
 #include <climits>
 
 #include "paged_common.cuh"
@@ -531,9 +532,10 @@ struct StoreArgs {
 // memory in the page's layout and written with 16-byte stores (each part of a
 // unit is contiguous).
 //
-// What bounds it: 2 d element bytes read and d / 2 + 4 G written a token and
-// operand, and about 10 instructions a channel, which at that rate of bytes
-// fill the SMs' issue slots as well.
+// What bounds it: issue slots, at about 14 instructions a channel (59 % busy).
+// 1.93 M tokens of bf16, d = 128, kept at random from rows four times as long:
+// 325 us for 1.27 GB. Three CTAs an SM with a part's loads at its start: with
+// the next part's loads under way registers allow two, 406 us.
 template <int D, int QG, bool F32>
 __global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 3) paged_store_kernel(const StoreArgs a) {
   constexpr int G = D / QG, LT = D / 16, TPI = 32 / LT, ITER = kUnit / TPI, W = D / 32, LG = QG / 16;
@@ -667,6 +669,8 @@ struct LoadArgs {
 };
 
 // Warps take runs of 16 output rows; lane t finds the token of output row t.
+// What bounds it: the writes, 512 of 656 bytes a token at d = 128 in bf16. 1.93 M
+// tokens take 270 us; a fill of the 990 MB written takes 256 us (3.87 TB/s).
 template <int D, int QG, bool F32>
 __global__ void __launch_bounds__(kMoveWarps * 32, 4) paged_load_kernel(const LoadArgs a) {
   constexpr int G = D / QG, LT = D / 8, TPI = 32 / LT, ITER = kUnit / TPI, W = D / 32;
@@ -775,7 +779,7 @@ __device__ __forceinline__ void copy_page(uint8_t* dst, const uint8_t* src, int 
   }
 }
 
-// One CTA per destination row: the full pages gain a holder, the rest is copied.
+// One CTA per destination row: the full pages gain a holder, the rest is copied. Latency: 4.7 us for 288 rows.
 __global__ void __launch_bounds__(kRowThreads) paged_fork_kernel(const MoveArgs a) {
   const PageGeom& g = a.g;
   const int row = blockIdx.x;
@@ -803,7 +807,8 @@ __global__ void __launch_bounds__(kRowThreads) paged_fork_kernel(const MoveArgs 
   }
 }
 
-// Every page of a row into a new one: grid (rows, slices); a slice's CTA takes every gridDim.y-th page.
+// Every page of a row into a new one: grid (rows, slices); a slice's CTA takes every gridDim.y-th page. Bound by
+// HBM: 26 us for 137 MB moved (5.3 TB/s).
 __global__ void __launch_bounds__(kRowThreads) paged_copy_kernel(const MoveArgs a) {
   const PageGeom& g = a.g;
   const int row = blockIdx.x;
@@ -826,7 +831,8 @@ __global__ void __launch_bounds__(kRowThreads) paged_copy_kernel(const MoveArgs 
 
 // The kept tokens' codes and scales into the new pages, in units of 16 of the
 // tokens to be; a V row whose place differs in bit 1 has its halves swapped.
-// The lists change hands in paged_commit_kernel, when every token has moved.
+// The lists change hands in paged_commit_kernel, when every token has moved. 64-byte rows picked at random: 48 us for
+// half of 1.23 M tokens, DRAM delivering the source pages whole (168 MB for 88).
 __global__ void __launch_bounds__(kMoveWarps * 32) paged_compact_kernel(const MoveArgs a) {
   const PageGeom& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
