@@ -32,7 +32,7 @@
  *   m = bf16(min x),  s = bf16(f32((max x - m) / 15)) (0 unless max x > m),
  *   c = clamp(rint((x - m) / s), 0, 15) (halves to even, the quotient exact;
  *   0 where s = 0);  the value held is m + c s.
- * A group with a NaN or an infinity holds NaN.
+ * A group with a NaN or an infinity, or whose smallest value rounds to one, holds NaN.
  *
  * Page layout (kv_paged_page_bytes() bytes, G = head_dim / quant_group):
  *   K codes [P][d / 2 bytes], V codes [P][d / 2 bytes], K scales [P][G],
@@ -109,7 +109,7 @@ int kv_paged_rebuild(const kv_paged_shape* shape, const kv_paged_cache* cache, v
 
 /*
  * kv_paged_append — quantises tokens and stores them behind each row's last.
- *   K, V    : device, [n_src][d] dtype (both the same rows).
+ *   K, V    : device, [n_src][d] dtype (both the same rows; not looked at where n_src = 0).
  *   count   : device int32 [call rows], tokens of each row (0 or more; a
  *             negative count is 0), or NULL: n_each tokens a row.
  *   src_off : device int64 [call rows], the source row that a row's positions
@@ -150,7 +150,9 @@ int kv_paged_load(const kv_paged_shape* shape, const kv_paged_cache* cache, cons
  *   key gives out = 0 and lse = -infinity.
  *   q, out : device, [call rows][n_q][g][d] dtype (out may not overlap q).
  *   lse    : device float32 [call rows][n_q][g], or NULL.
- *   n_q * group <= KV_PAGED_MAX_QUERIES. Queries are finite.
+ *   n_q * group <= KV_PAGED_MAX_QUERIES. Queries are finite (one that is not spoils its own
+ *   output only) and values held are below 2^100 in magnitude (sums over larger ones may pass
+ *   float32's range); a NaN held reaches the queries that see it.
  * Results do not depend on where the pages lie; repeated calls give the same bits.
  * Errors: KV_ERR_ARG, KV_ERR_WORKSPACE, KV_ERR_CUDA.
  */

@@ -1089,7 +1089,7 @@ int kv_paged_append(const kv_paged_shape* shape, const kv_paged_cache* cache, co
   if (!paged_shape_ok(shape) || !cache_ok(cache)) return KV_ERR_ARG;
   PlanArgs p = {};
   if (!make_rows(*shape, seq, n_seq, layer0, n_lay, true, &p.dst)) return KV_ERR_ARG;
-  if (!aligned16(K) || !aligned16(V) || n_src < 0 || n_each < 0) return KV_ERR_ARG;
+  if (n_src < 0 || n_each < 0 || (n_src > 0 && (!aligned16(K) || !aligned16(V)))) return KV_ERR_ARG;
   if (count && !src_off) return KV_ERR_ARG;
   if (idx && (!src_off || !idx_off)) return KV_ERR_ARG;
   if (!ws_ok(*shape, *cache)) return KV_ERR_WORKSPACE;

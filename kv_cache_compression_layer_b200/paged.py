@@ -78,6 +78,13 @@ class PagedCache:
             return nullcontext()
         return torch.cuda.device(self.device)
 
+    def _on(self, stream):
+        if stream is None:
+            return self._here()
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        return torch.cuda.stream(stream)
+
     def _is(self, name: str, x: torch.Tensor, dtype, numel: int, at_least: bool = False):
         if x.dtype != dtype or x.device != self.device or not x.is_contiguous():
             raise ValueError(f"{name}: a contiguous {dtype} tensor on {self.device}")
@@ -156,15 +163,19 @@ class PagedCache:
                stream=None) -> torch.Tensor:
         """Attention of ``n_q`` query tokens a row, their own tokens appended before: q and out
         [call rows, n_q, group, head_dim] (any shape of as many elements), lse float32 [call rows,
-        n_q, group] or None. Returns out."""
+        n_q, group] or None. Returns out (made on ``stream`` if it is not given)."""
         l0, nl, n = self._call_rows(seqs, layers)
         R = n_q * self.shape.group
         self._is("q", q, self.dtype, n * R * self.shape.head_dim)
-        if out is None:
-            out = torch.empty_like(q)
-        self._is("out", out, self.dtype, q.numel())
         if lse is not None:
             self._is("lse", lse, torch.float32, n * R)
+        if out is None:
+            with self._on(stream):  # memory that `stream` may write to, whatever else is under way
+                out = torch.empty_like(q)
+        else:
+            self._is("out", out, self.dtype, q.numel())
+            if abs(out.data_ptr() - q.data_ptr()) < q.numel() * q.element_size():
+                raise ValueError("out overlaps q")
         with self._here():
             kv_paged_attn(self.shape, self.cache, seqs, q, out, lse, n_q, l0, nl, stream)
         return out
@@ -191,6 +202,8 @@ class PagedCache:
         self._is("idx", idx, torch.int32, idx.numel())
         self._is("idx_off", idx_off, torch.int64, n, at_least=True)
         self._is("count", count, torch.int32, n)
+        if idx.numel() == 0:
+            idx = count  # nothing is kept and idx not read, but an empty tensor has no address
         with self._here():
             kv_paged_compact(self.shape, self.cache, src, dst, idx, idx_off, count, stream)
 

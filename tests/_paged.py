@@ -189,18 +189,18 @@ class Model:
     def attention(self, q, row, n_q):
         """out, lse and the bounds of their errors for q [n_q * g, d] (float64) of a row.
 
-        The library's logits: products of 24-bit (f32) or 8-bit q with codes are exact, their sums run in float32
-        over d channels (for bf16 with 128 added to every code), so a logit is off by at most
-        (d + 16) 2^-23 sum |q| (128 s + 15 s + |m|) / sqrt d (the 128 s term for bf16 only): E. A probability is then
-        off by a factor within 2 E + 2^-20 (exp2 and the sum). For bf16 the products p s are rounded to bf16 (2^-8 of
-        a term p s c, c <= 15). Sums over n keys add a rounding each 16 keys, of terms up to 143 s (15 s + |m| for
-        f32). The result is rounded once to its type."""
+        The library's logits: q scaled by a power of two to fp16 (f32: in two parts, 2^-22 of it left over) times
+        codes less 8 is exact, the sums over d channels run in float32, and (8 s + m) times the sum of q's channels
+        is added: a logit is off by at most (d + 16) 2^-23 sum |q| (16 s + |m|) / sqrt d: E. A probability is then
+        off by a factor within 2 E + 2^-20 (exp2 and the sum). For bf16 the products p s are rounded to fp16: 2^-11
+        of a term 8 p s at most, or 2^-30 of the largest step (half a last place of the smallest fp16, where the
+        largest step has p s = 2^5 at least) times a code of 8, for each of n keys. Sums over n keys add a rounding
+        each 16 keys, of terms up to 16 s + |m|. The result is rounded once to its type."""
         sh, g, d = self.sh, self.sh.group, self.sh.head_dim
         f32 = sh.dtype == kv.KV_F32
         out, lse = np.zeros(q.shape), np.full(len(q), -np.inf)
         tol, tol_lse = np.full(q.shape, 0.0), np.zeros(len(q))
         K, V = self.K[row], self.V[row]
-        bias = 0.0 if f32 else 128.0
         for i in range(len(q)):
             n = self.len[row] - n_q + 1 + i // g
             if n <= 0:
@@ -212,13 +212,13 @@ class Model:
             z = p.sum()
             out[i] = p @ v[:, 0] / z
             lse[i] = mx + math.log(z)
-            E = ((d + 16) * 2.0 ** -23 * ((bias + 15) * k[:, 1] + np.abs(k[:, 2])) @ np.abs(q[i]) / math.sqrt(d)).max()
+            E = ((d + 16) * 2.0 ** -23 * (16 * k[:, 1] + np.abs(k[:, 2])) @ np.abs(q[i]) / math.sqrt(d)).max()
             top = np.abs(v[:, 0]).max(0)
             rel = 2 * E + 2.0 ** -20
-            acc = (n / 16 + 24) * 2.0 ** -23 * (((bias + 15) * v[:, 1] + np.abs(v[:, 2])).max(0))
+            acc = (n / 16 + 24) * 2.0 ** -23 * ((16 * v[:, 1] + np.abs(v[:, 2])).max(0))
             tol[i] = 2 * rel * top + acc
             if not f32:
-                tol[i] += 2.0 ** -8 * 15 * v[:, 1].max(0) * 1.01
+                tol[i] += 8 * v[:, 1].max(0) * 2.0 ** -11 + n * 2.0 ** -27 * v[:, 1].max()
             tol[i] += (2.0 ** -24 if f32 else 2.0 ** -8) * (np.abs(out[i]) + tol[i])
             tol_lse[i] = E + 2.0 ** -20 + 2.0 ** -22 * abs(lse[i])
         return out, lse, tol, tol_lse

@@ -286,3 +286,116 @@ def test_values_of_any_size(scale):
     out = torch.empty_like(q)
     cache.attend([0], q, out)
     m.check_attention(q, out, None, [0], 1)
+
+
+def test_a_padded_batch():
+    """Rows without tokens and queries that are not finite (padding) leave the other queries as they should be."""
+    rng = np.random.default_rng(18)
+    for dtype, g, n_q in ((kv.KV_BF16, 8, 1), (kv.KV_BF16, 4, 3), (kv.KV_F32, 2, 4)):
+        cache, m = pg.make(n_seqs=3, n_layers=1, heads=2, group=g, dtype=dtype, max_pages=8)
+        pg.fill(cache, m, [300, 77, 0, 0, 500, 1], rng)
+        R = g * n_q
+        q = queries(rng, m, list(range(6)), R, dtype, cache.device)
+        q[2:4] = float("nan")  # of a sequence without tokens
+        spoilt = {(0, 1): float("nan"), (1, R - 1): float("inf"), (4, 0): -float("inf")}
+        for at, x in spoilt.items():
+            q[at][::3] = x
+        out = cache.attend([0, 1, 2], q, n_q=n_q)
+        assert cache.read_status() == 0
+        Q, O = q.double().cpu().numpy(), out.double().cpu().numpy()
+        assert (O[2:4] == 0).all()
+        for r in (0, 1, 4, 5):
+            good = [i for i in range(R) if (r, i) not in spoilt]
+            x = Q[r].copy()
+            x[[i for i in range(R) if i not in good]] = 0
+            o, _, tol, _ = m.attention(x, r, n_q)
+            assert (np.abs(O[r] - o) <= tol)[good].all()
+
+
+def test_longest_row():
+    """2^26 keys (one list that names eight pages over and over): attended over, forked, full, freed."""
+    rng = np.random.default_rng(19)
+    base, m = pg.make(n_seqs=1, n_layers=1, heads=1, group=2, max_pages=8)
+    pg.fill(base, m, [512], rng)
+    n, dev = 1 << 26, base.device
+    sh = kv.make_paged_shape(2, 1, 1, 2, 128, kv.KV_BF16, 8, n // 64, 64, 64)
+    table = torch.zeros(2, n // 64, dtype=torch.int32, device=dev)
+    table[0] = torch.arange(n // 64, device=dev) % 8
+    cache = kv.PagedCache(sh, pages=base.pages, table=table, lens=torch.tensor([n, 0], dtype=torch.int32, device=dev))
+    cache.fork([0], [1])
+    q = queries(rng, m, [0], 2, 1, dev)
+    lse = torch.empty(2, 1, 2, device=dev)
+    o0 = cache.attend([0], q, lse=lse[0])
+    o1 = cache.attend([1], q, lse=lse[1])
+    assert cache.read_status() == 0 and torch.equal(o0, o1) and torch.equal(lse[0], lse[1])
+    o, z, tol, tol_z = m.attention(q[0].double().cpu().numpy(), 0, 1)
+    # sums as in Model.attention, over the keys that a block takes (two a multiprocessor at least), a rounding of l and
+    # of the base's sum for each key of a lane (32 of its keys are summed in lanes and warps of their own)
+    N = n / (2 * torch.cuda.get_device_properties(dev).multi_processor_count)
+    V = m.V[0]
+    rel = N / 32 * 2.0 ** -24
+    tol = tol + N / 16 * 2.0 ** -23 * (16 * V[:, 1] + np.abs(V[:, 2])).max(0) + N * 2.0 ** -27 * V[:, 1].max() \
+        + 2 * rel * np.abs(V[:, 0]).max(0)
+    assert (np.abs(o0[0].double().cpu().numpy() - o) <= tol).all()
+    z = z + np.log(n / 512)
+    assert (np.abs(lse[0, 0].double().cpu().numpy() - z) <= tol_z + rel + 2.0 ** -22 * np.abs(z)).all()
+    one = torch.zeros(1, 128, dtype=torch.bfloat16, device=dev)
+    cache.append([1], one, one)  # there is no place behind the last
+    assert cache.read_status() == kv.KV_DEV_CAPACITY and cache.lens.tolist() == [n, n]
+    cache.free([0])
+    assert cache.free_pages() == 0
+    cache.free([1])
+    assert cache.free_pages() == 8
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls over one workspace, replayed in turn with calls between them, give what they gave."""
+    rng = np.random.default_rng(20)
+    cache, m = pg.make(n_seqs=4, n_layers=2, heads=2, group=4, page=16, max_pages=60)
+    pg.fill(cache, m, rng.integers(1, 900, m.rows), rng)
+    sets = [[0, 1], [2], [3, 0, 2]]
+    q = [queries(rng, m, m.call_rows(s), 8, 1, cache.device) for s in sets]
+    want = [cache.attend(s, x, n_q=2) for s, x in zip(sets, q)]
+    outs = [torch.empty_like(x) for x in q]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for s, x, o in zip(sets[:2], q, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=st):
+            cache.attend(s, x, o, n_q=2)
+    for i in range(10):
+        for o in outs:
+            o.fill_(7)
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            graphs[i % 2].replay()
+            cache.attend(sets[2], q[2], outs[2], n_q=2)
+            graphs[1 - i % 2].replay()
+        torch.cuda.current_stream().wait_stream(st)
+        assert all(torch.equal(w, o) for w, o in zip(want, outs))
+
+
+def test_outputs_on_another_stream():
+    """An output that the call makes belongs to the stream it was given, so that work still under way on the current
+    one does not reach it."""
+    rng = np.random.default_rng(21)
+    cache, m = pg.make(n_seqs=1, n_layers=2, heads=2, group=8, max_pages=8)
+    pg.fill(cache, m, [500] * m.rows, rng)
+    q = queries(rng, m, m.call_rows([0]), 8, 1, cache.device)
+    want = cache.attend([0], q)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (st, st.cuda_stream):
+        held = torch.empty_like(q)
+        torch.cuda._sleep(50_000_000)  # some tens of milliseconds, then a write to memory that is free again by then
+        held.fill_(9)
+        del held
+        out = cache.attend([0], q, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    with pytest.raises(ValueError):
+        cache.attend([0], q, out=q)
+    two = torch.empty(2 * q.numel() - 8, dtype=q.dtype, device=q.device)
+    with pytest.raises(ValueError):
+        cache.attend([0], two[: q.numel()], out=two[q.numel() - 8:])

@@ -171,3 +171,31 @@ def test_rebuild_reports_bad_lists():
     assert other.read_status() == kv.KV_DEV_BOUNDS and other.free_pages() == cache.shape.n_pages
     other.free([0])  # the page that is none is not counted
     assert other.free_pages() == cache.shape.n_pages
+
+
+def test_nothing_to_store_and_nothing_kept():
+    """Calls whose sources or positions are empty tensors."""
+    rng = np.random.default_rng(6)
+    cache, m = pg.make(n_seqs=2, n_layers=1, heads=2, page=16)
+    pg.fill(cache, m, [20, 3, 0, 0], rng)
+    dev = cache.device
+    none = torch.empty(0, 128, dtype=torch.bfloat16, device=dev)
+    zero = torch.zeros(2, dtype=torch.int32, device=dev)
+    off = torch.zeros(3, dtype=torch.int64, device=dev)
+    idx = torch.empty(0, dtype=torch.int32, device=dev)
+    cache.append([0], none, none)
+    cache.append([0], none, none, count=zero, src_off=off)
+    cache.append([1], none, none, count=zero, src_off=off, idx=idx, idx_off=off)
+    m.check(cache)
+    cache.append([0], none, none, count=zero + 2, src_off=off)  # sources that do not exist
+    m.append([0, 1], [np.zeros((2, 128))] * 2, [np.zeros((2, 128))] * 2)
+    m.status |= kv.KV_DEV_RANGE
+    m.check(cache)
+    cache.compact([0], [1], idx, off, zero)
+    cache.compact([0], [0], idx, off, zero)
+    m.compact([0], [0], [np.array([], int)] * 2)
+    m.check(cache)
+    assert cache.free_pages() == cache.shape.n_pages
+    cache.load([0, 1], none, none, torch.zeros(5, dtype=torch.int64, device=dev))
+    cache.fork([0], [1])
+    m.check(cache)

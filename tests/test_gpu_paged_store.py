@@ -167,3 +167,20 @@ def test_bad_page_numbers_are_reported():
     torch.cuda.synchronize()
     changed = (cache.pages != pages).any(1).nonzero().flatten().tolist()
     assert changed in ([], [m.lists[1][1]])
+
+
+def test_a_group_that_rounds_to_infinity():
+    """float32 values above the largest bf16: as the smallest of a group they round to an infinity, and the group
+    holds NaN; as the largest they only make the step."""
+    cache, _ = pg.make(n_seqs=1, n_layers=1, heads=1, d=64, qg=32, dtype=kv.KV_F32)
+    top = float(np.finfo(np.float32).max)
+    x = torch.full((1, 64), top, device=cache.device)
+    x[0, 32:] = torch.arange(32, device=cache.device) / 31 * top
+    y = -x
+    cache.append([0], x, y)
+    K, V = torch.empty_like(x), torch.empty_like(x)
+    cache.load([0], K, V, torch.tensor([0, 1], device=cache.device))
+    assert cache.read_status() == 0
+    assert torch.isnan(K[0, :32]).all() and torch.isnan(V[0]).all()  # -top is the smallest of both groups of V
+    want = pg.quantise(x.double().cpu().numpy(), 32)[0][0, 32:]
+    assert np.array_equal(K[0, 32:].double().cpu().numpy(), want.astype(np.float32).astype(np.float64))
