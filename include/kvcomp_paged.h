@@ -150,9 +150,9 @@ int kv_paged_load(const kv_paged_shape* shape, const kv_paged_cache* cache, cons
  *   key gives out = 0 and lse = -infinity.
  *   q, out : device, [call rows][n_q][g][d] dtype (out may not overlap q).
  *   lse    : device float32 [call rows][n_q][g], or NULL.
- *   n_q * group <= KV_PAGED_MAX_QUERIES. Queries are finite (one that is not spoils its own
- *   output only) and values held are below 2^100 in magnitude (sums over larger ones may pass
- *   float32's range); a NaN held reaches the queries that see it.
+ *   n_q * group <= KV_PAGED_MAX_QUERIES. Queries are finite, and queries and values held below
+ *   2^100 in magnitude (sums over larger ones may pass float32's range); a query that is not
+ *   spoils its own output only, a NaN held the outputs of the queries that see it.
  * Results do not depend on where the pages lie; repeated calls give the same bits.
  * Errors: KV_ERR_ARG, KV_ERR_WORKSPACE, KV_ERR_CUDA.
  */

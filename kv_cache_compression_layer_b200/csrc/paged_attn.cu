@@ -2,29 +2,33 @@
 // cache (formats in include/kvcomp_paged.h).
 //
 // What bounds it: the codes and scales are read once, d + 8 G bytes a token
-// (144 at d = 128 and groups of 64), and unpacking them takes 182 of the 367
-// instructions that 16 keys cost, half of those on the logic pipe, which takes
-// one every other cycle. 192 rows of 6400 keys (g = 8): 51.5 us, 3.45 TB/s over
-// all, 4.8 TB/s while tiles last; the rest is the start (lengths, shares, first
-// tile: 4 us) and SMs that end up to 4 us apart. fp32: 65 us; 16 queries: 81 us;
-// d = 64: 32 us; one row of one key: 5.5 us.
+// (144 at d = 128 and groups of 64), and 16 keys cost 296 instructions, 118 of
+// them to unpack the codes, most on the logic pipe, which takes one every other
+// cycle. 192 rows of 6400 keys (g = 8): 49.8 us, 3.6 TB/s; a copy without the
+// loads took 44, one without the arithmetic 40 (of which 31 at the rate of
+// plain reads, the rest the start and the end: lengths, shares, first tile,
+// partials). fp32: 66 us; 16 queries: 74; groups of 32: 58; d = 64: 31; one row
+// of one key: 5.7 us.
 //
-// Products. A pair of codes becomes two fp16 with one logic instruction and
-// one addition: bits 0-3 of a 16-bit half or-ed into 0x6400 are the number
-// 1024 + c, bits 4-7 or-ed into 0x5400 the number 64 + c; less 1032 or 72 they
-// are c - 8, exactly. With a group's step s and base m taken out of the sums,
-// and b = m + 8 s,
-//   q.k = sum_g s_g (q.(c - 8))_g + b_g (sum of q over g),
-//   sum_j p_j v_j = sum_j p'_j (c_j - 8) + sum_j p_j b_j,   p'_j = p_j s_j.
-// (Keeping an offset in the codes and subtracting it from the sums would save
-// the additions, but the tensor cores drop what lies below a running sum's last
-// bit: with 256 the outputs of 6400 keys were 0.7 % off.)
-// q is scaled by a power of two per query that brings its largest channel to
-// [256, 512), so a bf16 q is held exactly but for channels 2^22 below that; p'
-// is rounded to fp16 (2^-11 of a term) and scaled by a power of two that keeps
-// a row's largest step below 2^6 (p stays below 2^8), which follows a larger
-// step as the softmax's maximum follows a larger logit. For fp32 q and p' are
-// two fp16 each (22 bits).
+// Products. With a group's step s and base m taken out of the sums,
+//   q.k = sum_g s_g (q.c)_g + m_g (sum of q over g),
+//   sum_j p_j v_j = sum_j p'_j c_j + sum_j p_j m_j,   p'_j = p_j s_j.
+// A pair of codes becomes two fp16 with one logic instruction: alone in bits
+// 0-3 or 4-7 of a 16-bit half a code is the subnormal c 2^-24 or c 2^-20, and
+// mma takes subnormals. The 16 between the two kinds is taken from q's channels
+// and from the output's rows. q is scaled by a power of two per query that
+// brings its largest channel to [2^14, 2^15), p' by one that keeps a row's
+// largest step below 2^6 (p stays below 2^8) and that follows a larger step as
+// the softmax's maximum follows a larger logit; it is rounded to fp16 (2^-11 of
+// a term). mma sets its terms against the largest by their exponent fields and
+// drops what is 2^-25 below; a subnormal's field is that of 2^-14, so a term
+// loses up to 2^-15 of s times the largest q or p'. Both are below the
+// roundings of q's and out's own bf16 (rms error of out on 192 rows of 6400
+// keys: 1.81e-3 of it, 1.67e-3 from rounding it to bf16 alone).
+// For fp32 the codes are made c - 8, exactly (or-ed into 0x6400 they are 1024 +
+// c, into 0x5400 64 + c; one more addition each, m becomes m + 8 s), and q and
+// p' are two fp16 each (22 bits): no term of any size is lost. In bf16 these
+// additions took 49.8 us to 52.7, 16 queries' 74 to 82.
 // Both products have the cache as the 16-row operand (mma.sync m16n8k16: keys x
 // queries, then channels x queries), so up to 8 queries cost no padding; a
 // warp's fragments are one 16-byte load of K codes a key and 8-byte loads of V
@@ -121,17 +125,25 @@ __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t bits) {
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "n"(MASK), "r"(bits));
   return r;
 }
-// The four nibble pairs of x (bits 4 n and 16 + 4 n) as two fp16 each: c - 8.
+// The four nibble pairs of x (bits 4 n and 16 + 4 n) as two fp16 each: c - 8 (F32), or c 2^-24 (n even) and c 2^-20.
 struct CodeConst {
   uint32_t k10, k6;  // 1024 and 64 in both halves: the bits that make a number of a code
   uint32_t s10, s6;  // -1032 and -72: what makes it c - 8
 };
+template <bool F32>
 __device__ __forceinline__ void codes8(uint32_t x, const CodeConst& k, uint32_t (&c)[4]) {
   const uint32_t y = x >> 8;
-  c[0] = add2(pick<0x000f000fu>(x, k.k10), k.s10);
-  c[1] = add2(pick<0x00f000f0u>(x, k.k6), k.s6);
-  c[2] = add2(pick<0x000f000fu>(y, k.k10), k.s10);
-  c[3] = add2(pick<0x00f000f0u>(y, k.k6), k.s6);
+  if constexpr (F32) {
+    c[0] = add2(pick<0x000f000fu>(x, k.k10), k.s10);
+    c[1] = add2(pick<0x00f000f0u>(x, k.k6), k.s6);
+    c[2] = add2(pick<0x000f000fu>(y, k.k10), k.s10);
+    c[3] = add2(pick<0x00f000f0u>(y, k.k6), k.s6);
+  } else {
+    c[0] = x & 0x000f000fu;
+    c[1] = x & 0x00f000f0u;
+    c[2] = y & 0x000f000fu;
+    c[3] = y & 0x00f000f0u;
+  }
 }
 struct AttnArgs {
   PageGeom g;
@@ -390,9 +402,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
               for (int n = 0; n < 8; ++n) top = fmaxf(top, fabsf(x[w][n]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = max(-100, (int)(__float_as_uint(top) >> 23) - 127);  // 2^e <= top < 2^(e + 1)
-            const float up = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
-            const float down = a.scale2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+            // 2^e <= top < 2^(e + 1), within what the powers of two below can be
+            const int e = min(F32 ? 127 : 110, max(-100, (int)(__float_as_uint(top) >> 23) - 127));
+            const float up = __uint_as_float((uint32_t)(127 + (F32 ? 8 : 14) - e) << 23);
+            const float down = a.scale2 * __uint_as_float((uint32_t)(127 + (F32 ? -8 : 10) + e) << 23);
   #pragma unroll
             for (int z = 0; z < NG; ++z) sum[z] = 0.f;
   #pragma unroll
@@ -401,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
               for (int n = 0; n < 8; ++n) {
                 x[w][n] *= up;
                 sum[w * NG / W] += x[w][n];
+                if (!F32 && (n & 1)) x[w][n] *= 0.0625f;  // its code is 16 times the others' unit
               }
   #pragma unroll
               for (int p = 0; p < PARTS; ++p) {
@@ -417,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
             for (int z = 0; z < NG; ++z) {
               sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 1);
               sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 2);
-              if (tig == 0) meta[qi * (NG + 1) + z] = sum[z];
+              if (tig == 0) meta[qi * (NG + 1) + z] = F32 ? sum[z] : sum[z] * 0x1p-24f;
             }
             if (tig == 0) meta[qi * (NG + 1) + NG] = down;
           }
@@ -563,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           uint32_t c0[4], c1[4];
-          codes8(kw[0][w], kc, c0);
-          codes8(kw[1][w], kc, c1);
+          codes8<F32>(kw[0][w], kc, c0);
+          codes8<F32>(kw[1][w], kc, c1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -577,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         for (int x = 0; x < NG; ++x)
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const float sc = lo_f(ks[z][x]), ad = fmaf(8.f, sc, hi_f(ks[z][x]));
+            const float sc = lo_f(ks[z][x]), ad = F32 ? fmaf(8.f, sc, hi_f(ks[z][x])) : hi_f(ks[z][x]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -677,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
             float ps[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const float sc = lo_f(vs[u][x >> 1][z]), ba = fmaf(8.f, sc, hi_f(vs[u][x >> 1][z]));
+              const float sc = lo_f(vs[u][x >> 1][z]), ba = F32 ? fmaf(8.f, sc, hi_f(vs[u][x >> 1][z])) : hi_f(vs[u][x >> 1][z]);
               ps[x] = po[x] * sc;
               if constexpr (MASKED) {
                 off[nt][z][x & 1] += seen[x] ? p[x] * ba : 0.f;  // a token that another query sees may be NaN
@@ -715,8 +729,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
           const uint32_t xx = __byte_perm(vw[0][h >> 1], vw[1][h >> 1], sel);
           const uint32_t yy = __byte_perm(vw[2][h >> 1], vw[3][h >> 1], sel);
           uint32_t c0[4], c1[4];
-          codes8(xx, kc, c0);
-          codes8(yy, kc, c1);
+          codes8<F32>(xx, kc, c0);
+          codes8<F32>(yy, kc, c1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -735,7 +749,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       const uint8_t* stage = smem + st * S::kStage;
       const int tok = t * kTile + warp * 16;
       // both halves at once where every query sees all of them and the registers allow (16 queries spill, 192 rows of
-      // 6400 keys, g = 16, 102 us against 81; 8 queries with groups of 32, 62.3 against 60.9)
+      // 6400 keys, g = 16, 82 us against 74; 8 queries with groups of 32, 60.7 against 58; 8 with groups of 64, 49.8 against
+      // 53.5 one after the other)
       constexpr int U = NT == 1 && (NG < 4 || F32) ? 2 : 1;
       if (tok + 64 + 16 <= lim_min) {
 #pragma unroll 1
@@ -756,6 +771,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
 
     // ---- the CTA leaves the row: the warps' sums are joined
     const float inv = 1.f / om;
+    const float ue = F32 ? 1.f : 0x1p24f, uo = F32 ? 1.f : 0x1p20f;  // the codes' units, even and odd channels
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -772,8 +788,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         for (int h = 0; h < W; ++h) {
           const float add = off[nt][h * NG / W][x];
           *reinterpret_cast<float4*>(obuf + (warp * NQ + qi) * S::kORow + 32 * h + 4 * grp) =
-              make_float4(fmaf(O[nt][2 * h][x], inv, add), fmaf(O[nt][2 * h][2 + x], inv, add),
-                          fmaf(O[nt][2 * h + 1][x], inv, add), fmaf(O[nt][2 * h + 1][2 + x], inv, add));
+              make_float4(fmaf(O[nt][2 * h][x] * ue, inv, add), fmaf(O[nt][2 * h][2 + x] * uo, inv, add),
+                          fmaf(O[nt][2 * h + 1][x] * ue, inv, add), fmaf(O[nt][2 * h + 1][2 + x] * uo, inv, add));
         }
         if (grp == 0) ml[warp * NQ + qi] = make_float2(m2[nt][x], l[nt][x]);
       }

@@ -190,12 +190,15 @@ class Model:
         """out, lse and the bounds of their errors for q [n_q * g, d] (float64) of a row.
 
         The library's logits: q scaled by a power of two to fp16 (f32: in two parts, 2^-22 of it left over) times
-        codes less 8 is exact, the sums over d channels run in float32, and (8 s + m) times the sum of q's channels
-        is added: a logit is off by at most (d + 16) 2^-23 sum |q| (16 s + |m|) / sqrt d: E. A probability is then
-        off by a factor within 2 E + 2^-20 (exp2 and the sum). For bf16 the products p s are rounded to fp16: 2^-11
-        of a term 8 p s at most, or 2^-30 of the largest step (half a last place of the smallest fp16, where the
-        largest step has p s = 2^5 at least) times a code of 8, for each of n keys. Sums over n keys add a rounding
-        each 16 keys, of terms up to 16 s + |m|. The result is rounded once to its type."""
+        codes is exact, the sums over d channels run in float32, and the base (f32: and 8 steps) times the sum of q's
+        channels is added: a logit is off by at most (d + 16) 2^-23 sum |q| (16 s + |m|) / sqrt d. For bf16 the codes
+        are subnormals, c 2^-24, whose products count as 2^-14 times q in the matrix unit's alignment: of each of the
+        d products and d / 16 running sums what is below 2^-25 of that, 2^-15 s max |q|, may be lost. E is the sum. A
+        probability is then off by a factor within 2 E + 2^-20 (exp2 and the sum). For bf16 the products p s are
+        rounded to fp16: 2^-11 of a term 15 p s at most, or 2^-30 of the largest step (half a last place of the
+        smallest fp16, where the largest step has p s = 2^5 at least) times a code of 15, for each of n keys; and of
+        the 17 terms of 16 keys 2^-15 of the largest p s each is lost, 17 / 16 2^-11 of the sum of p s. Sums over n
+        keys add a rounding each 16 keys, of terms up to 16 s + |m|. The result is rounded once to its type."""
         sh, g, d = self.sh, self.sh.group, self.sh.head_dim
         f32 = sh.dtype == kv.KV_F32
         out, lse = np.zeros(q.shape), np.full(len(q), -np.inf)
@@ -213,12 +216,14 @@ class Model:
             out[i] = p @ v[:, 0] / z
             lse[i] = mx + math.log(z)
             E = ((d + 16) * 2.0 ** -23 * (16 * k[:, 1] + np.abs(k[:, 2])) @ np.abs(q[i]) / math.sqrt(d)).max()
+            if not f32:
+                E += 17 / 16 * d * 2.0 ** -15 * np.abs(q[i]).max() * k[:, 1].max() / math.sqrt(d)
             top = np.abs(v[:, 0]).max(0)
             rel = 2 * E + 2.0 ** -20
             acc = (n / 16 + 24) * 2.0 ** -23 * ((16 * v[:, 1] + np.abs(v[:, 2])).max(0))
             tol[i] = 2 * rel * top + acc
             if not f32:
-                tol[i] += 8 * v[:, 1].max(0) * 2.0 ** -11 + n * 2.0 ** -27 * v[:, 1].max()
+                tol[i] += (15 + 17 / 16) * 2.0 ** -11 * v[:, 1].max(0) + n * 15 * 2.0 ** -30 * v[:, 1].max()
             tol[i] += (2.0 ** -24 if f32 else 2.0 ** -8) * (np.abs(out[i]) + tol[i])
             tol_lse[i] = E + 2.0 ** -20 + 2.0 ** -22 * abs(lse[i])
         return out, lse, tol, tol_lse
