@@ -376,7 +376,10 @@ __device__ __forceinline__ Quantised quantise_fast(const float (&x)[16], float m
       unpack2(fma2(add2(y, f2(-magic, -magic)), n1, q), a, b);
       dev = fmaxf(dev, fmaxf(fabsf(a), fabsf(b)));
     }
-    unpack2(fma2(v, n1, add2(t, m2)), e0, e1);  // 0 where t is exact
+    // both 0 where t is exact; the first is not 0 where it was rounded and |x| <= |m|, the second where |x| >= |m|
+    unpack2(fma2(v, n1, add2(t, m2)), e0, e1);
+    off |= __float_as_uint(e0) | __float_as_uint(e1);
+    unpack2(add2(fma2(v, n1, t), m2), e0, e1);
     off |= __float_as_uint(e0) | __float_as_uint(e1);
     res.w[n >> 3] = (res.w[n >> 3] << 4) + __float_as_uint(y1);
     res.w[n >> 3] = (res.w[n >> 3] << 4) + __float_as_uint(y0);

@@ -17,6 +17,18 @@ def bf16(x):
     return torch.from_numpy(np.ascontiguousarray(np.asarray(x, np.float32))).to(torch.bfloat16).double().numpy()
 
 
+def rounded(x, dtype):
+    """float64 -> dtype, rounded once (torch and numpy pass through float32, which rounds a bf16 twice where a base far
+    below the step decides a half: m = 9e-10, c s = a half of bf16's last place): to float32 with what is left over
+    kept in the last bit, then to bf16."""
+    f = x.astype(np.float32)
+    if dtype == torch.bfloat16:
+        rest = np.isfinite(x) & (f.astype(np.float64) != x)
+        f = np.where(rest & (np.abs(f.astype(np.float64)) > np.abs(x)), np.nextafter(f, np.float32(0)), f)
+        f = np.where(rest, (f.view(np.uint32) | 1).view(np.float32), f)
+    return torch.from_numpy(np.ascontiguousarray(f)).to(dtype)
+
+
 def quantise(x, qg):
     """x [n, d] float64 -> values held [n, d], steps and bases spread over the channels [n, d]."""
     n, d = x.shape
@@ -181,8 +193,8 @@ class Model:
         want = [torch.full_like(K, 7.0).cpu(), torch.full_like(K, 9.0).cpu()]
         for r, o in zip(rows, off):
             for w, x in zip(want, (self.K[r], self.V[r])):
-                w[int(o):int(o) + self.len[r]] = torch.from_numpy(x[:, 0].astype(np.float32)).to(dt)
-        # m + c s in float32 is one rounding of the value held (c s is exact); float64 -> float32 the same one
+                w[int(o):int(o) + self.len[r]] = rounded(x[:, 0], dt)
+        # c s is exact, so m + c s is rounded once
         for w, got in zip(want, (K, V)):
             torch.testing.assert_close(got.cpu(), w, rtol=0, atol=0, equal_nan=True)
 

@@ -184,3 +184,23 @@ def test_a_group_that_rounds_to_infinity():
     assert torch.isnan(K[0, :32]).all() and torch.isnan(V[0]).all()  # -top is the smallest of both groups of V
     want = pg.quantise(x.double().cpu().numpy(), 32)[0][0, 32:]
     assert np.array_equal(K[0, 32:].double().cpu().numpy(), want.astype(np.float32).astype(np.float64))
+
+
+@pytest.mark.parametrize("dtype", [kv.KV_BF16, kv.KV_F32])
+def test_channels_far_apart(dtype):
+    """Groups that hold zeros and channels 2^-10 to 2^-40 of the rest, next to halves between codes: x - m is
+    rounded in float32 there, and the codes are still those of exact arithmetic."""
+    rng = np.random.default_rng(12)
+    n, d = 512, 128
+    x = rng.integers(-30, 31, (n, d)) * 0.5  # steps and halves that are met exactly
+    tiny = rng.random((n, d)) < 0.2
+    x = np.where(tiny, rng.normal(size=(n, d)) * 2.0 ** rng.integers(-40, -9, (n, 1)), x)
+    x[rng.random((n, d)) < 0.1] = 0.0
+    x[:, 0], x[:, 1] = 0.0, 15.0  # m = 0 or below, steps of a power of two among them
+    x[: n // 2] = np.abs(x[: n // 2])
+    x = pg.bf16(x)
+    for qg in (32, 128):
+        cache, m = pg.make(n_seqs=1, n_layers=1, heads=1, d=d, qg=qg, page=16, max_pages=64, dtype=dtype)
+        m.append([0], [x], [-x])
+        cache.append([0], pg.up(x, dtype, cache.device), pg.up(-x, dtype, cache.device))
+        m.check(cache)
