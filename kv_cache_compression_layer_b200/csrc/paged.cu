@@ -10,6 +10,7 @@
 // device wait, no atomics whose order shows: a page's count is an integer sum
 // and the bitmap a set. The plan is a chain of dependent loads and block sums
 // of one CTA, 5 to 10 us; the other kernels are bound by the bytes they move.
+#include <atomic>
 #include <climits>
 
 #include "paged_common.cuh"
@@ -280,32 +281,28 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 __device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 __device__ __forceinline__ uint32_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
-// What a lane holds of a quantised group: the codes of its 16 channels,
+// What a lane holds of a quantised group: the codes of its 32 channels,
 // channel 8 i + n in bits 4 n of w[i], and the packed (s, m).
 struct Quantised {
-  uint32_t w[2], scale;
+  uint32_t w[4], scale;
 };
 
 // The same by the definition, in float64: the quotient's rounding does not
-// reach a half (x, m and s have at most 24, 8 and 8 bits). A call, so that the
+// reach a half (x, m and s have at most 24, 8 and 8 bits). Calls, so that the
 // common path keeps its registers and its place in the instruction cache.
-__device__ __noinline__ Quantised quantise_exact(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
-                                                 float x7, float x8, float x9, float x10, float x11, float x12,
-                                                 float x13, float x14, float x15, float mx, float m) {
-  Quantised r;
-  r.w[0] = r.w[1] = 0u;
-  r.scale = 0x7fff7fffu;  // (NaN, NaN)
-  if (!(fabsf(mx) < INFINITY && fabsf(m) < INFINITY)) return r;
-  const float s = mx > m ? bf16_round((float)(((double)mx - (double)m) / 15.0)) : 0.f;
-  r.scale = bf16_bits(s) | (__float_as_uint(m) & 0xffff0000u);
-  if (s == 0.f) return r;
-  const float x[16] = {x0, x1, x2, x3, x4, x5, x6, x7, x8, x9, x10, x11, x12, x13, x14, x15};
+__device__ __noinline__ float step_exact(float mx, float m) {  // NaN: the group holds NaN
+  if (!(fabsf(mx) < INFINITY && fabsf(m) < INFINITY)) return __uint_as_float(0x7fffffffu);
+  return mx > m ? bf16_round((float)(((double)mx - (double)m) / 15.0)) : 0.f;
+}
+__device__ __noinline__ uint32_t codes_exact(float4 a, float4 b, float m, float s) {
+  const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t w = 0;
 #pragma unroll
-  for (int n = 0; n < 16; ++n) {
+  for (int n = 0; n < 8; ++n) {
     const double q = ((double)x[n] - (double)m) / (double)s;
-    r.w[n >> 3] |= (uint32_t)rint(fmin(fmax(q, 0.0), 15.0)) << (4 * (n & 7));
+    w |= (uint32_t)rint(fmin(fmax(q, 0.0), 15.0)) << (4 * n);
   }
-  return r;
+  return w;
 }
 
 // Two float32 in one register pair, and the packed operations on them.
@@ -333,20 +330,48 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// Quantises the 16 channels that a lane holds of a group with largest value mx
-// and base m (bf16 of the smallest), to exact arithmetic's result. The step:
-// the float32 product is off by a few of its last bits, which matters next to
-// the middle of two bf16. The codes: x - m is exact in float32 unless the two
-// lie far apart, and q follows from a reciprocal by one correction with the
-// exact remainder. An exact quotient k + 1/2 comes out as that; another
-// differs from it by the last bit of x - m over s at least, which is more than
-// half the last bit of q by 1 part in 255 (s has 8 bits), so it comes out on
-// its own side. What this does not cover goes to quantise_exact: a step next to
-// a middle, tiny, zero or not finite; an x - m that was rounded (bf16: rare;
-// F32: mostly, then only a quotient within 1e-5 of a half matters).
+// Where 16-byte piece q of a part lies in shared memory: a lane's N pieces
+// follow each other, and eight lanes' fall on different banks.
+template <int N>
+__device__ __forceinline__ int piece_at(int q) {
+  return q ^ ((q >> 3) & (N - 1));
+}
+
+// Channels 8 i .. 8 i + 7 of the 32 that start at piece q of a part in shared memory.
 template <bool F32>
-__device__ __forceinline__ Quantised quantise_fast(const float (&x)[16], float mx, float m) {
-  Quantised res;
+__device__ __forceinline__ void eight(const uint4* part, int q, int i, float4& a, float4& b) {
+  if constexpr (F32) {
+    a = *reinterpret_cast<const float4*>(part + piece_at<8>(q + 2 * i));
+    b = *reinterpret_cast<const float4*>(part + piece_at<8>(q + 2 * i + 1));
+  } else {
+    uint4 u;  // in order: taken early, they cost more registers than there are
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "r"(smem_u32(part + piece_at<4>(q + i)))
+                 : "memory");
+    a = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                    __uint_as_float(u.y & 0xffff0000u));
+    b = make_float4(__uint_as_float(u.z << 16), __uint_as_float(u.z & 0xffff0000u), __uint_as_float(u.w << 16),
+                    __uint_as_float(u.w & 0xffff0000u));
+  }
+}
+
+// Quantises the 32 channels that a lane holds of a group with largest value mx
+// and base m (bf16 of the smallest), to exact arithmetic's result; false where
+// it may not be. The step: the float32 product is off by a few of its last
+// bits, which matters next to the middle of two bf16. The codes: x - m is exact
+// in float32 unless the two lie far apart, and q follows from a reciprocal by
+// one correction with the exact remainder. An exact quotient k + 1/2 comes out
+// as that; another differs from it by the last bit of x - m over s at least,
+// which is more than half the last bit of q by 1 part in 255 (s has 8 bits), so
+// it comes out on its own side. What this does not cover: a step next to a
+// middle, tiny, zero or not finite; an x - m that was rounded. For F32 that is
+// common, and matters only with a quotient within 1e-5 of a half. bf16 numbers
+// are multiples of 2^-8 of themselves, so none is rounded while the smallest
+// magnitude but 0 (`least`: of these 32) is 2^-16 of mx - m or more; where it is
+// not, each channel is looked at.
+template <bool F32>
+__device__ __forceinline__ bool quantise_fast(const uint4* part, int q0, float mx, float m, float least, Quantised& res) {
   const float magic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits of the sum
   const float f = __fmul_rn(__fsub_rn(mx, m), 1.f / 15.f);
   const float s = bf16_round(f);
@@ -356,43 +381,69 @@ __device__ __forceinline__ Quantised quantise_fast(const float (&x)[16], float m
                  n1 = f2(-1.f, -1.f);
   uint32_t off = 0;
   float dev = 0.f;
-  res.w[0] = res.w[1] = 0u;
 #pragma unroll
-  for (int n = 14; n >= 0; n -= 2) {
-    const uint64_t v = f2(x[n], x[n + 1]);
-    const uint64_t t = add2(v, nm2);
-    const uint64_t q0 = mul2(t, r2);
-    uint64_t q = fma2(fma2(q0, ns2, t), r2, q0);
-    if (F32) {  // the base may be above the smallest
-      float a, b;
-      unpack2(q, a, b);
-      q = f2(fmaxf(a, 0.f), fmaxf(b, 0.f));
+  for (int i = 0; i < 4; ++i) {
+    float4 a, b;
+    eight<F32>(part, q0, i, a, b);
+    const uint64_t x[4] = {f2(a.x, a.y), f2(a.z, a.w), f2(b.x, b.y), f2(b.z, b.w)};
+    uint32_t w = 0;
+#pragma unroll
+    for (int n = 3; n >= 0; --n) {
+      const uint64_t v = x[n];
+      const uint64_t t = add2(v, nm2);
+      const uint64_t p = mul2(t, r2);
+      uint64_t q = fma2(fma2(p, ns2, t), r2, p);
+      if (F32) {  // the base may be above the smallest
+        float c, d;
+        unpack2(q, c, d);
+        q = f2(fmaxf(c, 0.f), fmaxf(d, 0.f));
+      }
+      const uint64_t y = add2(q, g2);
+      float y0, y1;
+      unpack2(y, y0, y1);
+      if (F32) {
+        float c, d, e0, e1;
+        unpack2(fma2(add2(y, f2(-magic, -magic)), n1, q), c, d);
+        dev = fmaxf(dev, fmaxf(fabsf(c), fabsf(d)));
+        // both 0 where t is exact; the first is not 0 where it was rounded and |x| <= |m|, the second where |x| >= |m|
+        unpack2(fma2(v, n1, add2(t, m2)), e0, e1);
+        off |= __float_as_uint(e0) | __float_as_uint(e1);
+        unpack2(add2(fma2(v, n1, t), m2), e0, e1);
+        off |= __float_as_uint(e0) | __float_as_uint(e1);
+      }
+      w = (w << 4) + __float_as_uint(y1);
+      w = (w << 4) + __float_as_uint(y0);
     }
-    const uint64_t y = add2(q, g2);
-    float y0, y1, e0, e1;
-    unpack2(y, y0, y1);
-    if (F32) {
-      float a, b;
-      unpack2(fma2(add2(y, f2(-magic, -magic)), n1, q), a, b);
-      dev = fmaxf(dev, fmaxf(fabsf(a), fabsf(b)));
-    }
-    // both 0 where t is exact; the first is not 0 where it was rounded and |x| <= |m|, the second where |x| >= |m|
-    unpack2(fma2(v, n1, add2(t, m2)), e0, e1);
-    off |= __float_as_uint(e0) | __float_as_uint(e1);
-    unpack2(add2(fma2(v, n1, t), m2), e0, e1);
-    off |= __float_as_uint(e0) | __float_as_uint(e1);
-    res.w[n >> 3] = (res.w[n >> 3] << 4) + __float_as_uint(y1);
-    res.w[n >> 3] = (res.w[n >> 3] << 4) + __float_as_uint(y0);
+    res.w[i] = w - 0x3F400000u;  // what the eight shifted exponents of `magic` (0x4B400000) add up to
   }
-  res.w[0] -= 0x3F400000u;  // what the eight shifted exponents of `magic` (0x4B400000) add up to
-  res.w[1] -= 0x3F400000u;
   res.scale = bf16_bits(f) | (__float_as_uint(m) & 0xffff0000u);
-  const bool covered = f > 1e-30f && f < 1e37f && (__float_as_uint(f) & 0xffffu) - 0x7fe0u > 0x40u &&
-                       ((off & 0x7fffffffu) == 0u || (F32 && dev <= 0.49999f));
-  if (!covered)
-    res = quantise_exact(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], x[8], x[9], x[10], x[11], x[12], x[13], x[14],
-                         x[15], mx, m);
-  return res;
+  if (!F32 && (least < __fsub_rn(mx, m) * 0x1p-16f || (m != 0.f && fabsf(m) < __fsub_rn(mx, m) * 0x1p-16f))) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      float4 a, b;
+      eight<F32>(part, q0, i, a, b);
+      const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {  // t is exact where both are 0
+        const float t = __fsub_rn(x[n], m);
+        off |= __float_as_uint(__fsub_rn(__fadd_rn(t, m), x[n])) | __float_as_uint(__fadd_rn(__fsub_rn(t, x[n]), m));
+      }
+    }
+  }
+  return f > 1e-30f && f < 1e37f && (__float_as_uint(f) & 0xffffu) - 0x7fe0u > 0x40u &&
+         ((off & 0x7fffffffu) == 0u || (F32 && dev <= 0.49999f));
+}
+
+template <bool F32>
+__device__ __forceinline__ void quantise_exact(const uint4* part, int q, float mx, float m, Quantised& res) {
+  const float s = step_exact(mx, m);
+  res.scale = s == s ? bf16_bits(s) | (__float_as_uint(m) & 0xffff0000u) : 0x7fff7fffu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float4 a, b;
+    eight<F32>(part, q, i, a, b);
+    res.w[i] = s > 0.f ? codes_exact(a, b, m, s) : 0u;
+  }
 }
 
 __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
@@ -406,70 +457,74 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
-// 16 channels of a row: loaded with 16-byte loads, quantised with the LG
-// consecutive lanes that hold the rest of their group (NaN and infinities
-// reach the group's largest or smallest).
-template <bool F32>
-struct Row16;
-template <>
-struct Row16<false> {
-  uint4 a, b;
-  __device__ __forceinline__ void load(const void* base, long long off) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + off);
-    a = p[0];
-    b = p[1];
-  }
-  __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
-  template <int LG>
-  __device__ __forceinline__ Quantised quantise() const {
-    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t hi = u[0], lo = u[0];
-    float x[16];
+// The number of smaller magnitude of each pair (its sign is the product's).
+__device__ __forceinline__ uint32_t min2_abs(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Of N rows (the 32 channels from piece q + n * dq on each): the largest value
+// of the group that the LG consecutive lanes hold, and bf16 of its smallest
+// (NaN and infinities reach them); bf16: the least magnitude of the 32 channels.
+template <bool F32, int LG, int N>
+__device__ __forceinline__ void group_ends(const uint4* part, int q, int dq, float (&mx)[N], float (&m)[N],
+                                           float (&least)[N]) {
+  if constexpr (F32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      hi = max2_nan(hi, u[i]);
-      lo = min2_nan(lo, u[i]);
-      x[2 * i] = __uint_as_float(u[i] << 16);
-      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-    lo ^= 0x80008000u;  // the largest and the negated smallest share a register
-    uint32_t v = max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
+    for (int n = 0; n < N; ++n) {
 #pragma unroll
-    for (int o = 1; o < LG; o <<= 1) v = max2_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return quantise_fast<false>(x, __uint_as_float(v << 16), __uint_as_float((v & 0xffff0000u) ^ 0x80000000u));
-  }
-};
-template <>
-struct Row16<true> {
-  float4 v[4];
-  __device__ __forceinline__ void load(const void* base, long long off) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
+      for (int i = 0; i < 4; ++i) {
+        float4 a, b;
+        eight<true>(part, q + n * dq, i, a, b);
+        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (i == 0) mx[n] = m[n] = x[0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = p[i];
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  template <int LG>
-  __device__ __forceinline__ Quantised quantise() const {
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[4 * i] = v[i].x, x[4 * i + 1] = v[i].y, x[4 * i + 2] = v[i].z, x[4 * i + 3] = v[i].w;
-    float mx = x[0], mn = x[0];
-#pragma unroll
-    for (int n = 1; n < 16; ++n) {
-      mx = max_nan(mx, x[n]);
-      mn = min_nan(mn, x[n]);
+        for (int k = 0; k < 8; ++k) {
+          mx[n] = max_nan(mx[n], x[k]);
+          m[n] = min_nan(m[n], x[k]);
+        }
+      }
     }
 #pragma unroll
-    for (int o = 1; o < LG; o <<= 1) {
-      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    for (int o = 1; o < LG; o <<= 1)
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        mx[n] = max_nan(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], o));
+        m[n] = min_nan(m[n], __shfl_xor_sync(0xffffffffu, m[n], o));
+      }
+#pragma unroll
+    for (int n = 0; n < N; ++n) m[n] = bf16_round(m[n]);
+  } else {
+    uint32_t v[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      uint32_t hi = 0, lo = 0, near = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 u = part[piece_at<4>(q + n * dq + i)];
+        const uint32_t h = max2_nan(max2_nan(u.x, u.y), max2_nan(u.z, u.w));
+        const uint32_t l = min2_nan(min2_nan(u.x, u.y), min2_nan(u.z, u.w));
+        hi = i ? max2_nan(hi, h) : h;
+        lo = i ? min2_nan(lo, l) : l;
+        const uint32_t k = min2_abs(min2_abs(u.x, u.y), min2_abs(u.z, u.w));
+        near = i ? min2_abs(near, k) : k;
+      }
+      least[n] = fminf(fabsf(__uint_as_float(near << 16)), fabsf(__uint_as_float(near & 0xffff0000u)));
+      lo ^= 0x80008000u;  // the largest and the negated smallest share a register
+      v[n] = max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
     }
-    return quantise_fast<true>(x, mx, bf16_round(mn));
+#pragma unroll
+    for (int o = 1; o < LG; o <<= 1)
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] = max2_nan(v[n], __shfl_xor_sync(0xffffffffu, v[n], o));
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      mx[n] = __uint_as_float(v[n] << 16);
+      m[n] = __uint_as_float((v[n] & 0xffff0000u) ^ 0x80000000u);
+    }
   }
-};
+}
 
 // (x & mask) | bits in one instruction: it takes one constant, so the other comes in a register.
 template <uint32_t MASK>
@@ -529,24 +584,44 @@ struct StoreArgs {
 };
 
 // Warps take runs of units of 16 tokens (a unit starts at a multiple of 16 of
-// the row's tokens, so it lies in one page). D / 16 lanes hold a token's row, 16
+// the row's tokens, so it lies in one page). D / 32 lanes hold a token's row, 32
 // channels each (so that a group's scale, worked out in each of its lanes, is
-// shared by 16 channels). A unit's K, then its V, is quantised into shared
-// memory in the page's layout and written with 16-byte stores (each part of a
-// unit is contiguous).
+// shared by 32 channels). The next part's (K's or V's) 16-byte pieces are on
+// their way into shared memory while a part is quantised, and the next unit's
+// place and source positions are read a part before those are needed. A part is
+// quantised into shared memory in the page's layout and written with 16-byte
+// stores (each part of a unit is contiguous).
 //
-// What bounds it: issue slots, at about 14 instructions a channel (59 % busy).
-// 1.93 M tokens of bf16, d = 128, kept at random from rows four times as long:
-// 325 us for 1.27 GB. Three CTAs an SM with a part's loads at its start: with
-// the next part's loads under way registers allow two, 406 us.
+// What bounds it: instructions, and their latency where registers allow 16 warps
+// an SM. 1.93 M tokens of bf16, d = 128, kept at random from rows four times as
+// long: 295 us for 1.27 GB (4.3 TB/s). A copy that did not quantise took 215.
+// With 16 channels a lane loaded into registers, rows one after the other, three
+// CTAs an SM: 325 us; with these side by side at 80 registers (they spill) 385,
+// at 128 and two CTAs 340.
 template <int D, int QG, bool F32>
-__global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 3) paged_store_kernel(const StoreArgs a) {
-  constexpr int G = D / QG, LT = D / 16, TPI = 32 / LT, ITER = kUnit / TPI, W = D / 32, LG = QG / 16;
-  constexpr int kCode = kUnit * D / 2, kScale = kUnit * G * 4;
-  __shared__ __align__(16) uint8_t stage[kMoveWarps][kCode + kScale];
+struct StoreSmem {
+  static constexpr int kPieces = F32 ? 8 : 4;                     // of a lane's 32 channels
+  static constexpr int kSrc = kUnit * D * (F32 ? 4 : 2);          // a part's source rows, piece by piece
+  static constexpr int kCode = kUnit * D / 2, kScale = kUnit * (D / QG) * 4;
+  static constexpr int kWarp = 2 * kSrc + kCode + kScale, kBytes = kMoveWarps * kWarp;
+};
+
+// By what the RC 16-byte pieces of token t's codes change places in the stage.
+template <int RC>
+__device__ __forceinline__ int turn(int t) {
+  return RC == 4 ? (t >> 1) & 3 : (t >> 2) & 1;
+}
+
+template <int D, int QG, bool F32>
+__global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 2) paged_store_kernel(const StoreArgs a) {
+  using S = StoreSmem<D, QG, F32>;
+  constexpr int G = D / QG, W = D / 32, TPI = 32 / W, ITER = kUnit / TPI, LG = QG / 32;
+  constexpr int kCode = S::kCode, PC = S::kPieces;
+  constexpr int RC = D / 2 / 16;  // 16-byte pieces of a token's codes
+  extern __shared__ __align__(128) uint8_t smem[];
   const PageGeom& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int l = lane % LT, sub = lane / LT;
+  const int l = lane % W, sub = lane / W;
   pdl_launch_dependents();
   pdl_wait();
   const int n_rows = a.rows.n_rows;
@@ -554,21 +629,22 @@ __global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 3) paged_store_kern
   const long long nw = (long long)gridDim.x * kMoveWarps, w = (long long)blockIdx.x * kMoveWarps + warp;
   const int u0 = (int)(w * total / nw), u1 = (int)((w + 1) * total / nw);
   if (u0 >= u1) return;
-  uint8_t* st = stage[warp];
+  uint4* in = reinterpret_cast<uint4*>(smem + warp * S::kWarp);
+  uint8_t* st = smem + warp * S::kWarp + 2 * S::kSrc;
   int bad = 0;
   // the row of the next unit: its units [row_u0, row_u1), plan and source
   int row = -1, row_u0 = 0, row_u1 = -1;
   RowPlan p{};
   long long base = 0, at = 0;
 
-  // A unit: where it goes (page, place of its first token, its new tokens [f, e)) and, in lane t, the element offset of
-  // the source row of its token t (-1: none).
+  // A unit: where it goes (page, place of its first token, its new tokens [f, e)).
   struct Unit {
     int page, place, f, e;
-    long long src;
   };
-  auto unit_at = [&](int u) {
-    Unit x;
+  Unit now, next{};
+  int spot = 0;        // in lane t, the source position of the next unit's token t
+  bool isnew = false;  // the next unit's page is new
+  auto locate = [&](int u) {
     if (u >= row_u1) {
       row = find_unit_row(a.unit, n_rows, u);
       row_u0 = a.unit[row];
@@ -578,83 +654,110 @@ __global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 3) paged_store_kern
       if (a.idx) at = a.idx_off[row];
     }
     const int pos0 = (p.old / kUnit + u - row_u0) * kUnit;
-    x.f = max(p.old - pos0, 0);
-    x.e = min(kUnit, p.old + p.n - pos0);
+    next.f = max(p.old - pos0, 0);
+    next.e = min(kUnit, p.old + p.n - pos0);
     const int j = pos0 >> g.log_p;
-    x.place = pos0 & (g.P - 1);
-    if (j >= p.fresh) {
-      x.page = a.take[p.take + j - p.fresh];
-      if (x.place == 0 && lane == 0) claim_page(a.c, g, table_row(a.rows, row), j, x.page);
-    } else {
-      x.page = a.c.table[(size_t)table_row(a.rows, row) * g.max_pages + j];
-      if (x.page < 0 || x.page >= g.n_pages) {
-        bad |= KV_DEV_BOUNDS;
-        x.f = x.e = 0;  // nothing of it is stored
-        x.page = 0;
-      }
+    next.place = pos0 & (g.P - 1);
+    isnew = j >= p.fresh;
+    next.page = isnew ? a.take[p.take + j - p.fresh] : a.c.table[(size_t)table_row(a.rows, row) * g.max_pages + j];
+    spot = pos0 + lane - p.old;
+    if (a.idx && lane >= next.f && lane < next.e) spot = a.idx[at + spot];
+  };
+  // The element offset of the source row of the next unit's token t in lane t (-1: none); enters a new page.
+  auto settle = [&](int u) {
+    if (isnew) {
+      if (next.place == 0 && lane == 0)
+        claim_page(a.c, g, table_row(a.rows, row), ((p.old / kUnit + u - row_u0) * kUnit) >> g.log_p, next.page);
+    } else if (next.page < 0 || next.page >= g.n_pages) {
+      bad |= KV_DEV_BOUNDS;
+      next.f = next.e = 0;  // nothing of it is stored
+      next.page = 0;
     }
-    x.src = -1;
-    if (lane >= x.f && lane < x.e) {
-      const int t = pos0 + lane - p.old;
-      const long long src = base + (a.idx ? (long long)a.idx[at + t] : (long long)t);
-      if (src < 0 || src >= a.n_src) bad |= KV_DEV_RANGE;
-      else x.src = src * D;
+    if (lane < next.f || lane >= next.e) return -1ll;
+    const long long src = base + spot;
+    if (src >= 0 && src < a.n_src) return src * D;
+    bad |= KV_DEV_RANGE;
+    return -1ll;
+  };
+  auto fetch = [&](uint4* part, const void* from, long long src) {
+    constexpr int PPR = W * PC;  // pieces of a row
+#pragma unroll
+    for (int x = 0; x < kUnit * PPR / 32; ++x) {
+      const int q = x * 32 + lane;
+      const long long s = __shfl_sync(0xffffffffu, src, q / PPR);
+      uint4* to = part + piece_at<PC>(q);
+      if (s >= 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)),
+                     "l"(static_cast<const uint8_t*>(from) + s * (F32 ? 4 : 2) + q % PPR * 16)
+                     : "memory");
+      else
+        *to = make_uint4(0, 0, 0, 0);
     }
-    return x;
   };
 
-  Unit now{};
-  long long off[ITER];  // of this lane's tokens' channels
+  locate(u0);
+  long long src = settle(u0);
+  now = next;
+  fetch(in, a.K, src);
 #pragma unroll 1
   for (int i = 2 * u0; i < 2 * u1; ++i) {
     const bool v = i & 1;  // the unit's V, else its K
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();  // the part is there, the previous one is done with
+    const uint4* part = in + (v ? S::kSrc / 16 : 0);
+    const Unit here = now;
     if (!v) {
-      now = unit_at(i >> 1);
-#pragma unroll
-      for (int it = 0; it < ITER; ++it) {
-        const long long s = __shfl_sync(0xffffffffu, now.src, it * TPI + sub);
-        off[it] = s < 0 ? -1 : s + 16 * l;
-      }
+      fetch(in + S::kSrc / 16, a.V, src);
+      if (i + 2 < 2 * u1) locate((i >> 1) + 1);
+    } else if (i + 1 < 2 * u1) {
+      src = settle((i >> 1) + 1);
+      now = next;
+      fetch(in, a.K, src);
     }
-    Row16<F32> cur[ITER];
+    // the rows side by side, what the fast way does not cover afterwards: a branch for each would keep them apart
+    float mx[ITER], m[ITER], least[ITER];
+    Quantised z[ITER];
+    unsigned hard = 0;
+    group_ends<F32, LG>(part, lane * PC, 32 * PC, mx, m, least);
+#pragma unroll
+    for (int it = 0; it < ITER; ++it)
+      if (!quantise_fast<F32>(part, (it * 32 + lane) * PC, mx[it], m[it], least[it], z[it])) hard |= 1u << it;
+    if (hard) {
+#pragma unroll
+      for (int it = 0; it < ITER; ++it)
+        if (hard >> it & 1) quantise_exact<F32>(part, (it * 32 + lane) * PC, mx[it], m[it], z[it]);
+    }
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
-      if (off[it] >= 0) cur[it].load(v ? a.V : a.K, off[it]);
-      else cur[it].zero();
-    }
-    __syncwarp();  // the previous part has left the stage
-#pragma unroll
-    for (int it = 0; it < ITER; ++it) {
+      // channels 32 l + 8 i + n are word (i, l) of K, or the 16-bit words (2 i, l) and (2 i + 1, l) of V, in places
+      // swapped by the token's bit 1; 16-byte pieces of the stage are turned by the token so that banks differ
       const int t = it * TPI + sub;
-      const Quantised z = cur[it].template quantise<LG>();
-      // channels 16 l .. 16 l + 15 lie in channels 32 (l / 2) .. of the row, from its first or second half on
-      if (!v) {  // words (t, w), t = channel % 32 / 8
-        uint32_t* sk = reinterpret_cast<uint32_t*>(st) + t * (D / 8) + 2 * (l & 1) * W + (l >> 1);
-        sk[0] = z.w[0];
-        sk[W] = z.w[1];
-      } else {  // 16-bit words (p, h), p = channel % 32 / 4, in places swapped by the token's bit 1
-        const int pv = (4 * (l & 1)) ^ ((t & 2) << 1);
-        uint16_t* sv = reinterpret_cast<uint16_t*>(st) + t * (D / 4) + pv * W + (l >> 1);
-        sv[0] = (uint16_t)z.w[0];
-        sv[W] = (uint16_t)(z.w[0] >> 16);
-        sv[2 * W] = (uint16_t)z.w[1];
-        sv[3 * W] = (uint16_t)(z.w[1] >> 16);
+      uint8_t* row_st = st + t * (D / 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at_byte = v ? ((2 * i) ^ ((t & 2) << 1)) * (2 * W) + 2 * l : i * (4 * W) + 4 * l;
+        uint8_t* to = row_st + (((at_byte >> 4) ^ turn<RC>(t)) << 4) + (at_byte & 15);
+        if (!v) {
+          *reinterpret_cast<uint32_t*>(to) = z[it].w[i];
+        } else {
+          reinterpret_cast<uint16_t*>(to)[0] = (uint16_t)z[it].w[i];
+          reinterpret_cast<uint16_t*>(to)[W] = (uint16_t)(z[it].w[i] >> 16);
+        }
       }
-      if (l % LG == 0) reinterpret_cast<uint32_t*>(st + kCode)[t * G + l / LG] = z.scale;
+      if (l % LG == 0) reinterpret_cast<uint32_t*>(st + kCode)[t * G + l / LG] = z[it].scale;
     }
     __syncwarp();
-    uint8_t* pg = a.c.pages + (size_t)now.page * g.bytes;
-    constexpr int RC = D / 2 / 16;  // 16-byte pieces of a token's codes
+    uint8_t* pg = a.c.pages + (size_t)here.page * g.bytes;
     const uint4* ss = reinterpret_cast<const uint4*>(st);
-    uint4* d = reinterpret_cast<uint4*>(pg + (v ? g.v : 0) + now.place * (D / 2));
+    uint4* d = reinterpret_cast<uint4*>(pg + (v ? g.v : 0) + here.place * (D / 2));
     const uint32_t* sx = reinterpret_cast<const uint32_t*>(st + kCode);
-    uint32_t* dx = reinterpret_cast<uint32_t*>(pg + (v ? g.vs : g.ks)) + now.place * G;
+    uint32_t* dx = reinterpret_cast<uint32_t*>(pg + (v ? g.vs : g.ks)) + here.place * G;
 #pragma unroll
     for (int x = lane; x < kUnit * RC; x += 32)
-      if (x >= now.f * RC && x < now.e * RC) d[x] = ss[x];
+      if (x >= here.f * RC && x < here.e * RC) d[x] = ss[x ^ turn<RC>(x / RC)];
 #pragma unroll
     for (int x = lane; x < (kUnit * G + 31) / 32 * 32; x += 32)
-      if (x >= now.f * G && x < now.e * G) dx[x] = sx[x];
+      if (x >= here.f * G && x < here.e * G) dx[x] = sx[x];
   }
   if (bad) atomicOr(a.c.status, bad);
 }
@@ -782,7 +885,8 @@ __device__ __forceinline__ void copy_page(uint8_t* dst, const uint8_t* src, int 
   }
 }
 
-// One CTA per destination row: the full pages gain a holder, the rest is copied. Latency: 4.7 us for 288 rows.
+// One CTA per destination row: the full pages gain a holder, the rest is copied. Latency: a fork of
+// 288 rows of 1500 tokens and its freeing take 11 us.
 __global__ void __launch_bounds__(kRowThreads) paged_fork_kernel(const MoveArgs a) {
   const PageGeom& g = a.g;
   const int row = blockIdx.x;
@@ -1001,10 +1105,11 @@ bool make_rows(const kv_paged_shape& sh, const int32_t* seq, int32_t n, int laye
 // Launch whose set-up overlaps the previous kernel's tail. Every kernel here waits for that kernel before it touches
 // memory, and reads with plain loads (the read-only path may not see what a kernel that was still running wrote).
 template <class... P, class... A>
-int launch(void (*k)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+int launch_smem(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1013,11 +1118,30 @@ int launch(void (*k)(P...), dim3 grid, int threads, cudaStream_t st, A... args) 
   cfg.numAttrs = 1;
   return cuda_status(cudaLaunchKernelEx(&cfg, k, P(args)...));
 }
+template <class... P, class... A>
+int launch(void (*k)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  return launch_smem(k, grid, threads, 0, st, args...);
+}
 
+template <int D, int QG, bool F32>
+int store_with(int blocks, const StoreArgs& a, cudaStream_t st) {
+  using S = StoreSmem<D, QG, F32>;
+  auto k = paged_store_kernel<D, QG, F32>;
+  static std::atomic<unsigned long long> ready{0};  // devices on which the kernel may take its shared memory
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KV_ERR_CUDA;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
+      return KV_ERR_CUDA;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int cap = (F32 ? 1 : 2) * sm_count();  // all resident
+  return launch_smem(k, blocks < cap ? blocks : cap, kMoveWarps * 32, S::kBytes, st, a);
+}
 template <int D, int QG>
-int store_as(bool f32, int grid, const StoreArgs& a, cudaStream_t st) {
-  return f32 ? launch(paged_store_kernel<D, QG, true>, grid, kMoveWarps * 32, st, a)
-             : launch(paged_store_kernel<D, QG, false>, grid, kMoveWarps * 32, st, a);
+int store_as(bool f32, int blocks, const StoreArgs& a, cudaStream_t st) {
+  return f32 ? store_with<D, QG, true>(blocks, a, st) : store_with<D, QG, false>(blocks, a, st);
 }
 template <int D, int QG>
 int load_as(bool f32, int grid, const LoadArgs& a, cudaStream_t st) {
@@ -1108,8 +1232,8 @@ int kv_paged_append(const kv_paged_shape* shape, const kv_paged_cache* cache, co
   StoreArgs a = {p.g, p.dst, p.c, K, V, n_src, n_each, src_off, idx, idx_off, w.plan, w.unit, w.take};
   // a unit per warp while that leaves SMs idle; the batch's units are known on the device only, n_src bounds them
   const long long warps = n_src / kUnit + 2ll * p.dst.n_rows;
-  const long long want = (warps + kMoveWarps - 1) / kMoveWarps, cap = 3ll * sm_count();  // all resident
-  const int grid = (int)(want < cap ? want : cap);
+  const long long want = (warps + kMoveWarps - 1) / kMoveWarps;
+  const int grid = (int)(want < INT_MAX ? want : INT_MAX);
   const bool f32 = shape->dtype == KV_F32;
   if (shape->head_dim == 64) return shape->quant_group == 32 ? store_as<64, 32>(f32, grid, a, st) : store_as<64, 64>(f32, grid, a, st);
   return shape->quant_group == 32   ? store_as<128, 32>(f32, grid, a, st)
