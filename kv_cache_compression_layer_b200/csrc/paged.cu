@@ -594,7 +594,7 @@ struct StoreArgs {
 //
 // What bounds it: instructions, and their latency where registers allow 16 warps
 // an SM. 1.93 M tokens of bf16, d = 128, kept at random from rows four times as
-// long: 295 us for 1.27 GB (4.3 TB/s). A copy that did not quantise took 215.
+// long: 283 us for 1.27 GB (4.5 TB/s). A copy that did not quantise took 215.
 // With 16 channels a lane loaded into registers, rows one after the other, three
 // CTAs an SM: 325 us; with these side by side at 80 registers (they spill) 385,
 // at 128 and two CTAs 340.
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 2) paged_store_kern
     spot = pos0 + lane - p.old;
     if (a.idx && lane >= next.f && lane < next.e) spot = a.idx[at + spot];
   };
-  // The element offset of the source row of the next unit's token t in lane t (-1: none); enters a new page.
+  // The byte offset of the source row of the next unit's token t in lane t (-1: none); enters a new page.
   auto settle = [&](int u) {
     if (isnew) {
       if (next.place == 0 && lane == 0)
@@ -675,23 +675,21 @@ __global__ void __launch_bounds__(kMoveWarps * 32, F32 ? 1 : 2) paged_store_kern
     }
     if (lane < next.f || lane >= next.e) return -1ll;
     const long long src = base + spot;
-    if (src >= 0 && src < a.n_src) return src * D;
+    if (src >= 0 && src < a.n_src) return src * (D * (F32 ? 4 : 2));
     bad |= KV_DEV_RANGE;
     return -1ll;
   };
+  constexpr int PPR = W * PC;  // pieces of a row, at most 32
+  const int mine = lane % PPR * 16;
   auto fetch = [&](uint4* part, const void* from, long long src) {
-    constexpr int PPR = W * PC;  // pieces of a row
+    const uint8_t* base = static_cast<const uint8_t*>(from) + mine;
 #pragma unroll
     for (int x = 0; x < kUnit * PPR / 32; ++x) {
-      const int q = x * 32 + lane;
-      const long long s = __shfl_sync(0xffffffffu, src, q / PPR);
-      uint4* to = part + piece_at<PC>(q);
-      if (s >= 0)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)),
-                     "l"(static_cast<const uint8_t*>(from) + s * (F32 ? 4 : 2) + q % PPR * 16)
-                     : "memory");
-      else
-        *to = make_uint4(0, 0, 0, 0);
+      const long long s = __shfl_sync(0xffffffffu, src, x * (32 / PPR) + lane / PPR);
+      // a piece that has no source is zeros: none of its bytes are read
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(part + piece_at<PC>(x * 32 + lane))),
+                   "l"(s >= 0 ? base + s : reinterpret_cast<const uint8_t*>(a.unit)), "r"(s >= 0 ? 16 : 0)
+                   : "memory");
     }
   };
 
