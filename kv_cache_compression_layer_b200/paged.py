@@ -82,7 +82,8 @@ class PagedCache:
         if stream is None:
             return self._here()
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=self.device)
+            stream = (torch.cuda.ExternalStream(stream, device=self.device) if stream
+                      else torch.cuda.default_stream(self.device))
         return torch.cuda.stream(stream)
 
     def _is(self, name: str, x: torch.Tensor, dtype, numel: int, at_least: bool = False):

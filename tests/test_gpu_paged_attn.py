@@ -394,6 +394,12 @@ def test_outputs_on_another_stream():
         out = cache.attend([0], q, stream=stream)
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+    assert cache._on(0).stream == torch.cuda.default_stream(cache.device)  # 0 names the default stream, not a new one
+    with torch.cuda.stream(st):
+        st.wait_stream(torch.cuda.default_stream())
+        out = cache.attend([0], q, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
     with pytest.raises(ValueError):
         cache.attend([0], q, out=q)
     two = torch.empty(2 * q.numel() - 8, dtype=q.dtype, device=q.device)
