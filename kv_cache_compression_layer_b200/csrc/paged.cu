@@ -9,7 +9,7 @@
 // page, enters the page into the row's list, its count and the bitmap. No
 // device wait, no atomics whose order shows: a page's count is an integer sum
 // and the bitmap a set. The plan is a chain of dependent loads and block sums
-// of one CTA, 5 to 10 us; the other kernels are bound by the bytes they move.
+// of one CTA, 2.5 us for 288 rows; what bounds the others stands at each.
 #include <atomic>
 #include <climits>
 
