@@ -146,8 +146,13 @@ int kv_paged_load(const kv_paged_shape* shape, const kv_paged_cache* cache, cons
  * their own tokens appended before the call:
  *   query token t of a row sees keys 0 .. len - n_q + t;
  *   out = softmax(q K^T / sqrt(d)) V over them,  lse = log sum exp(q K^T / sqrt(d))
- *   with K and V the values held (float32 accumulation). A query that sees no
- *   key gives out = 0 and lse = -infinity.
+ *   with K and V the values held. A query that sees no key gives out = 0 and
+ *   lse = -infinity. Sums are float32's: a logit is off by at most
+ *   (d + 16) 2^-23 sum_c |q_c| (16 s_c + |m_c|) / sqrt d (s and m the step and
+ *   base that channel c is held with). KV_BF16 rounds a key's weight times its V
+ *   step to fp16, 2^-11 of it (to 16 bits where V steps of a row lie far apart),
+ *   KV_F32 to 24 bits; channels, tokens and queries of any size beside each other
+ *   cost one another nothing.
  *   q, out : device, [call rows][n_q][g][d] dtype (out may not overlap q).
  *   lse    : device float32 [call rows][n_q][g], or NULL.
  *   n_q * group <= KV_PAGED_MAX_QUERIES. Queries are finite, and queries and values held below

@@ -2,33 +2,30 @@
 // cache (formats in include/kvcomp_paged.h).
 //
 // What bounds it: the codes and scales are read once, d + 8 G bytes a token
-// (144 at d = 128 and groups of 64), and 16 keys cost 296 instructions, 118 of
+// (144 at d = 128 and groups of 64), and 16 keys cost some 370 instructions, 128 of
 // them to unpack the codes, most on the logic pipe, which takes one every other
-// cycle. 192 rows of 6400 keys (g = 8): 49.8 us, 3.6 TB/s; a copy without the
-// loads took 44, one without the arithmetic 40 (of which 31 at the rate of
-// plain reads, the rest the start and the end: lengths, shares, first tile,
-// partials). fp32: 66 us; 16 queries: 74; groups of 32: 58; d = 64: 31; one row
-// of one key: 5.7 us.
+// cycle. 192 rows of 6400 keys (g = 8): 54.3 us, 3.3 TB/s (a form that let terms
+// be cut at 2^-15 of the largest took 49). fp32: 77 us; 16 queries: 83; groups of
+// 32: 68; d = 64: 34.5; one row of one key: 5.9 us.
 //
 // Products. With a group's step s and base m taken out of the sums,
 //   q.k = sum_g s_g (q.c)_g + m_g (sum of q over g),
 //   sum_j p_j v_j = sum_j p'_j c_j + sum_j p_j m_j,   p'_j = p_j s_j.
-// A pair of codes becomes two fp16 with one logic instruction: alone in bits
-// 0-3 or 4-7 of a 16-bit half a code is the subnormal c 2^-24 or c 2^-20, and
-// mma takes subnormals. The 16 between the two kinds is taken from q's channels
-// and from the output's rows. q is scaled by a power of two per query that
-// brings its largest channel to [2^14, 2^15), p' by one that keeps a row's
-// largest step below 2^6 (p stays below 2^8) and that follows a larger step as
-// the softmax's maximum follows a larger logit; it is rounded to fp16 (2^-11 of
-// a term). mma sets its terms against the largest by their exponent fields and
-// drops what is 2^-25 below; a subnormal's field is that of 2^-14, so a term
-// loses up to 2^-15 of s times the largest q or p'. Both are below the
-// roundings of q's and out's own bf16 (rms error of out on 192 rows of 6400
-// keys: 1.81e-3 of it, 1.67e-3 from rounding it to bf16 alone).
-// For fp32 the codes are made c - 8, exactly (or-ed into 0x6400 they are 1024 +
-// c, into 0x5400 64 + c; one more addition each, m becomes m + 8 s), and q and
-// p' are two fp16 each (22 bits): no term of any size is lost. In bf16 these
-// additions took 49.8 us to 52.7, 16 queries' 74 to 82.
+// Operands are 16-bit, sums float32. A pair of codes becomes 128 + c in two bf16
+// with a shift and a logic instruction, c - 8 with one addition more (the bases
+// then count m - 128 s or m + 8 s).
+// Logits: bf16 queries are taken as they are times 128 + c, whose sums' last bits
+// are 2^-23 of 143 sum |q| at most; centred codes took 192 rows of 6400 keys from
+// 54.8 to 58.8 us. fp32 queries are three bf16 each (24 bits) times c - 8.
+// Outputs: p' is rounded to fp16 (2^-11 of a term) times c - 8 in fp16 (or-ed into
+// 0x6400 a code is 1024 + c, into 0x5400 64 + c), under a scale for each group of
+// channels, a power of two that a row's first keys choose. fp16 reaches from 2^-24
+// to 2^16, so this holds while steps stay within 2^10 of each other; before the
+// first keys whose steps do not (each lane looks at one key's), the row's sums
+// drop their scales, and from there on p' is two bf16 (16 bits), which need none.
+// So it is for a row's last keys too, and for fp32 with three bf16, always: no
+// group, token or query costs another its bits. Two bf16 for all keys took 59.5
+// us, a scale for each query and group that follows its largest p' 60.5.
 // Both products have the cache as the 16-row operand (mma.sync m16n8k16: keys x
 // queries, then channels x queries), so up to 8 queries cost no padding; a
 // warp's fragments are one 16-byte load of K codes a key and 8-byte loads of V
@@ -64,6 +61,9 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kRowCost = 2;   // of starting and leaving a row, in tiles
 constexpr int kMinShare = 2;  // cost of a CTA's share, at least
 constexpr int kJoin = 8;      // partials joined at once
+// Steps times their scale that fp16 p' allow: weights are below 2^8, so p' stays below 2^15; the largest weight so far is 1
+// or more, so its p' is 2^-3 or more, 2^22 times what rounding to the smallest fp16 takes from another.
+constexpr float kReachLo = 0x1p-3f, kReachHi = 0x1p7f;
 constexpr float kGrow = 8.f;  // the running maximum moves when a logit passes it by this (log2 units)
 
 // Shared memory of a CTA: the ring of stages, the warps' outputs and (maximum,
@@ -78,41 +78,52 @@ struct Smem {
   static constexpr int kObuf = kStages * kStage;
   static constexpr int kMl = kObuf + kWarps * NQ * kORow * 4;
   static constexpr int kQ = kMl + kWarps * NQ * 8;
-  static constexpr int kFrag = NQ * D * (F32 ? 4 : 2), kQBytes = kFrag + NQ * (NG + 1) * 4;
+  static constexpr int kFrag = NQ * D * (F32 ? 6 : 2), kQBytes = kFrag + NQ * NG * 4;
   static constexpr int kBase = kQ + 2 * kQBytes;
   static constexpr int kLen = kBase + (kAttnRows + 1) * 4;
   static constexpr int kBar = (kLen + kAttnRows * 4 + 7) / 8 * 8;
   static constexpr int kBytes = kBar + (2 * kStages + 4) * 8 + 48;
 };
 
+// c += A B, A 16 x 16, B 16 x 8, both bf16, or (F16) fp16.
+template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// Two fp16 of a and b (lo in the low half), and what their rounding left of them.
+// Two bf16 of a and b (lo in the low half), and what their rounding left of them.
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ void rest2(uint32_t u, float& lo, float& hi) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-  lo -= f.x;
-  hi -= f.y;
-}
-__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ void rest2(uint32_t u, float& lo, float& hi) {
+  lo -= lo_f(u);
+  hi -= hi_f(u);
+}
+__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 __device__ __forceinline__ uint32_t add2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t add2_f16(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
@@ -125,24 +136,25 @@ __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t bits) {
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "n"(MASK), "r"(bits));
   return r;
 }
-// The four nibble pairs of x (bits 4 n and 16 + 4 n) as two fp16 each: c - 8 (F32), or c 2^-24 (n even) and c 2^-20.
+// The four nibble pairs of x (bits 4 n and 16 + 4 n) as two numbers c - 8 each, exactly: bf16, or (F16) fp16.
 struct CodeConst {
-  uint32_t k10, k6;  // 1024 and 64 in both halves: the bits that make a number of a code
-  uint32_t s10, s6;  // -1032 and -72: what makes it c - 8
+  uint32_t k7, s7;            // bf16: 128, which a code or-ed into makes 128 + c, and -136, in both halves
+  uint32_t k10, k6, s10, s6;  // fp16: 1024 and 64 (for a code in bits 4-7), -1032 and -72
 };
-template <bool F32>
+template <bool F16, bool CENTRED = true>
 __device__ __forceinline__ void codes8(uint32_t x, const CodeConst& k, uint32_t (&c)[4]) {
-  const uint32_t y = x >> 8;
-  if constexpr (F32) {
-    c[0] = add2(pick<0x000f000fu>(x, k.k10), k.s10);
-    c[1] = add2(pick<0x00f000f0u>(x, k.k6), k.s6);
-    c[2] = add2(pick<0x000f000fu>(y, k.k10), k.s10);
-    c[3] = add2(pick<0x00f000f0u>(y, k.k6), k.s6);
+  if constexpr (F16) {
+    const uint32_t y = x >> 8;
+    c[0] = add2_f16(pick<0x000f000fu>(x, k.k10), k.s10);
+    c[1] = add2_f16(pick<0x00f000f0u>(x, k.k6), k.s6);
+    c[2] = add2_f16(pick<0x000f000fu>(y, k.k10), k.s10);
+    c[3] = add2_f16(pick<0x00f000f0u>(y, k.k6), k.s6);
   } else {
-    c[0] = x & 0x000f000fu;
-    c[1] = x & 0x00f000f0u;
-    c[2] = y & 0x000f000fu;
-    c[3] = y & 0x00f000f0u;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      c[n] = pick<0x000f000fu>(x >> (4 * n), k.k7);
+      if constexpr (CENTRED) c[n] = add2(c[n], k.s7);
+    }
   }
 }
 struct AttnArgs {
@@ -151,7 +163,7 @@ struct AttnArgs {
   PagedCache c;
   int row0, n_rows;  // call rows of this launch
   int n_q, group, R; // R = n_q * group
-  float scale2;      // log2(e) / sqrt(d)
+  float scale2, inv_scale2;  // log2(e) / sqrt(d)
   const void* q;
   void* out;
   float* lse;
@@ -160,6 +172,9 @@ struct AttnArgs {
   unsigned long long limit_ns;
   CodeConst kc;  // an argument, so that the constants stay in registers
 };
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // The NG scales of a token.
 template <int NG>
@@ -237,7 +252,7 @@ __device__ __forceinline__ void put4(void* out, long long at, float4 o, float L)
         make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   else
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
-        make_uint2(pack2_bf16(o.x * inv, o.y * inv), pack2_bf16(o.z * inv, o.w * inv));
+        make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
 }
 __device__ __forceinline__ float lse_of(float M, float L) {
   return L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
@@ -246,7 +261,7 @@ __device__ __forceinline__ float lse_of(float M, float L) {
 template <int D, int NG, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2) paged_attn_kernel(const AttnArgs a) {
   using S = Smem<D, NG, NT, F32>;
-  constexpr int W = D / 32, NQ = S::NQ, PARTS = F32 ? 2 : 1, kStages = S::kStages;
+  constexpr int W = D / 32, NQ = S::NQ, QP = F32 ? 3 : 1, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   float* obuf = reinterpret_cast<float*>(smem + S::kObuf);
   float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
@@ -376,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
   #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const int qi = nt * 8 + grp;
-            float x[W][8], top = 0.f, sum[NG];
+            float x[W][8], sum[NG];
   #pragma unroll
             for (int w = 0; w < W; ++w) {
               const long long at = ((long long)(a.row0 + r) * a.R + q0 + qi) * D + 32 * w + 8 * tig;
@@ -397,43 +412,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
               }
             }
   #pragma unroll
-            for (int w = 0; w < W; ++w)
-  #pragma unroll
-              for (int n = 0; n < 8; ++n) top = fmaxf(top, fabsf(x[w][n]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^e <= top < 2^(e + 1), within what the powers of two below can be
-            const int e = min(F32 ? 127 : 110, max(-100, (int)(__float_as_uint(top) >> 23) - 127));
-            const float up = __uint_as_float((uint32_t)(127 + (F32 ? 8 : 14) - e) << 23);
-            const float down = a.scale2 * __uint_as_float((uint32_t)(127 + (F32 ? -8 : 10) + e) << 23);
-  #pragma unroll
             for (int z = 0; z < NG; ++z) sum[z] = 0.f;
   #pragma unroll
             for (int w = 0; w < W; ++w) {
   #pragma unroll
-              for (int n = 0; n < 8; ++n) {
-                x[w][n] *= up;
-                sum[w * NG / W] += x[w][n];
-                if (!F32 && (n & 1)) x[w][n] *= 0.0625f;  // its code is 16 times the others' unit
-              }
+              for (int n = 0; n < 8; ++n) sum[w * NG / W] += x[w][n];
   #pragma unroll
-              for (int p = 0; p < PARTS; ++p) {
+              for (int p = 0; p < QP; ++p) {
                 uint32_t f[4];  // a code pair holds channels n and n + 4
   #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                   f[n] = pack2(x[w][n], x[w][n + 4]);
                   rest2(f[n], x[w][n], x[w][n + 4]);
                 }
-                frag[((nt * PARTS + p) * W + w) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+                frag[((nt * QP + p) * W + w) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
               }
             }
   #pragma unroll
             for (int z = 0; z < NG; ++z) {
               sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 1);
               sum[z] += __shfl_xor_sync(0xffffffffu, sum[z], 2);
-              if (tig == 0) meta[qi * (NG + 1) + z] = F32 ? sum[z] : sum[z] * 0x1p-24f;
+              if (tig == 0) meta[qi * NG + z] = sum[z];
             }
-            if (tig == 0) meta[qi * (NG + 1) + NG] = down;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&q_full[k & 1]);
@@ -491,27 +491,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     }
     ok = wait(&q_full[k & 1], (k >> 1) & 1);
 
-    // query fragments, their sums by group, and what turns a sum into a logit in log2 units
-    uint32_t qf[NT][PARTS][W][4];
-    float qsum[NT][NG][2], unit[NT][2];
+    // query fragments and their sums by group
+    uint32_t qf[NT][QP][W][4];
+    float qsum[NT][NG][2];
     {
       const uint4* frag = reinterpret_cast<const uint4*>(smem + S::kQ + (k & 1) * S::kQBytes);
       const float* meta = reinterpret_cast<const float*>(smem + S::kQ + (k & 1) * S::kQBytes + S::kFrag);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p)
+        for (int p = 0; p < QP; ++p)
 #pragma unroll
           for (int w = 0; w < W; ++w) {
-            const uint4 u = frag[((nt * PARTS + p) * W + w) * 32 + lane];
+            const uint4 u = frag[((nt * QP + p) * W + w) * 32 + lane];
             qf[nt][p][w][0] = u.x, qf[nt][p][w][1] = u.y, qf[nt][p][w][2] = u.z, qf[nt][p][w][3] = u.w;
           }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {  // this lane's columns are queries 2 tig + c
-          const float* mq = meta + (nt * 8 + 2 * tig + c) * (NG + 1);
+          const float* mq = meta + (nt * 8 + 2 * tig + c) * NG;
 #pragma unroll
           for (int z = 0; z < NG; ++z) qsum[nt][z][c] = mq[z];
-          unit[nt][c] = mq[NG];
         }
       }
     }
@@ -541,13 +540,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       m2[nt][0] = m2[nt][1] = thr[nt][0] = thr[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    float om = 1.f, s_top = -1.f;  // scale of p', and the largest step that it is made for
-
-    // The warp's 16 keys of each of the halves u0 .. u0 + U - 1 of tile t in stage st; MASKED: some are hidden from
-    // some query.
+    float om[NG];         // the scales of p' and O by group of channels; 0: not yet chosen
+    bool wide = F32;      // no scale any more: steps lay too far apart
+#pragma unroll
+    for (int z = 0; z < NG; ++z) om[z] = F32 ? 1.f : 0.f;
+    // The warp's 16 keys of each of the halves u0 .. u0 + U - 1 of tile t in stage st; MASKED: some may be hidden from
+    // some query, and steps may lie apart (WIDE). False: not done, since they do.
     auto attend = [&](auto uu, auto mk, const uint8_t* st, int u0, int t) {
       constexpr int U = decltype(uu)::value;
-      constexpr bool MASKED = decltype(mk)::value;
+      constexpr bool MASKED = decltype(mk)::value, WIDE = MASKED || F32;
+      constexpr int PP = F32 ? 3 : WIDE ? 2 : 1;
       const int row0 = krow + 64 * u0;          // token of the tile in matrix row grp; row grp + 8 is 8 further
       const int key0 = t * kTile + row0;
       // ---- logits: rows keys, columns queries
@@ -577,21 +579,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           uint32_t c0[4], c1[4];
-          codes8<F32>(kw[0][w], kc, c0);
-          codes8<F32>(kw[1][w], kc, c1);
+          codes8<false, F32>(kw[0][w], kc, c0);
+          codes8<false, F32>(kw[1][w], kc, c1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int p = PARTS - 1; p >= 0; --p) {
-              mma(acc[nt][w * NG / W], c0[0], c1[0], c0[1], c1[1], qf[nt][p][w][0], qf[nt][p][w][1]);
-              mma(acc[nt][w * NG / W], c0[2], c1[2], c0[3], c1[3], qf[nt][p][w][2], qf[nt][p][w][3]);
+            for (int p = QP - 1; p >= 0; --p) {
+              mma<false>(acc[nt][w * NG / W], c0[0], c1[0], c0[1], c1[1], qf[nt][p][w][0], qf[nt][p][w][1]);
+              mma<false>(acc[nt][w * NG / W], c0[2], c1[2], c0[3], c1[3], qf[nt][p][w][2], qf[nt][p][w][3]);
             }
         }
 #pragma unroll
         for (int x = 0; x < NG; ++x)
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const float sc = lo_f(ks[z][x]), ad = F32 ? fmaf(8.f, sc, hi_f(ks[z][x])) : hi_f(ks[z][x]);
+            const float sc = lo_f(ks[z][x]), ad = fmaf(F32 ? 8.f : -128.f, sc, hi_f(ks[z][x]));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -622,32 +624,70 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
           }
         }
       // ---- softmax: the running maximum follows only when a logit passes it by far
-      bool grow = false;
+      bool grow = false, odd = false;
+      if constexpr (!F32) {
+        if (!wide) {  // this lane's key's steps
+          const int at = warp * 16 + (lane & 15) + 64 * (U == 2 ? lane >> 4 : u0);
+          uint32_t sw[NG];
+          load_scales<NG>(st + S::kVs + at * (NG * 4), sw);
+#pragma unroll
+          for (int z = 0; z < NG; ++z) {
+            const float x = lo_f(sw[z]) * om[z];
+            odd |= !(x >= kReachLo && x <= kReachHi);
+          }
+          if (MASKED) odd &= t * kTile + at < len;
+          grow = odd;
+        }
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 4; ++x) grow |= y[u][nt][x] > thr[nt][x & 1];
-      float s_max = 0.f;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int z = 0; z < NG; ++z) s_max = fmaxf(s_max, lo_f(vs[u][x][z]));
-      grow |= s_max > s_top;
       if (__any_sync(0xffffffffu, grow)) {
-        float fo = 1.f;
+        if constexpr (!F32) {
+          if (__any_sync(0xffffffffu, odd)) {
+            // the row's first keys choose the scales; steps that are out of reach end them
+            const bool first = om[0] == 0.f;
+            bool out = !first;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) s_max = fmaxf(s_max, __shfl_xor_sync(0xffffffffu, s_max, o));
-        if (s_max > s_top) {
-          // 2^e <= s_max < 2^(e + 1): p' is scaled by 2^(5 - e), at most 2^100; a step of 0 leaves the choice open
-          const int e = max(-95, (int)(__float_as_uint(s_max) >> 23) - 127);
-          const float now = __uint_as_float((uint32_t)(127 + 5 - e) << 23);
-          s_top = s_max == 0.f ? 0.f : __uint_as_float((uint32_t)(127 + e + 1) << 23);
-          fo = now * __frcp_rn(om);
-          om = now;
+            for (int z = 0; z < NG; ++z) {
+              float top = 0.f, low = INFINITY;
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  if (MASKED && key0 + 64 * u + 8 * x >= len) continue;
+                  const float sc = lo_f(vs[u][x][z]);
+                  top = fmaxf(top, sc);
+                  low = sc >= 0.f ? fminf(low, sc) : 0.f;  // NaN: no reach
+                }
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+              }
+              const float choice = pow2(4 - min(100, max(-96, (int)(__float_as_uint(top) >> 23) - 127)));
+              out |= !(top * choice <= kReachHi && low * choice >= kReachLo);
+              if (first) om[z] = choice;
+            }
+            if (out) {
+              wide = true;
+#pragma unroll
+              for (int z = 0; z < NG; ++z) {
+                const float inv = __frcp_rn(om[z]);
+                om[z] = 1.f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int h = 2 * z * W / NG; h < 2 * (z + 1) * W / NG; ++h)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) O[nt][h][x] *= inv;
+              }
+              if (!WIDE) return false;
+            }
+          }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -657,42 +697,41 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
             if constexpr (U == 2) mx = fmaxf(mx, fmaxf(y[1][nt][x], y[1][nt][2 + x]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float now = fmaxf(m2[nt][x], mx * unit[nt][x]);
-            const float f = now == m2[nt][x] ? 1.f : ex2_approx(m2[nt][x] - now), g2 = f * fo;
+            const float now = fmaxf(m2[nt][x], mx * a.scale2);
+            const float f = now == m2[nt][x] ? 1.f : ex2_approx(m2[nt][x] - now);
             m2[nt][x] = now;
-            thr[nt][x] = __fdividef(now + kGrow, unit[nt][x]);
+            thr[nt][x] = (now + kGrow) * a.inv_scale2;
             l[nt][x] *= f;
 #pragma unroll
             for (int z = 0; z < NG; ++z) off[nt][z][x] *= f;
 #pragma unroll
             for (int z = 0; z < 2 * W; ++z) {
-              O[nt][z][x] *= g2;
-              O[nt][z][2 + x] *= g2;
+              O[nt][z][x] *= f;
+              O[nt][z][2 + x] *= f;
             }
           }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        uint32_t b[NT][NG][PARTS][2];
+        uint32_t b[NT][NG][PP][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float p[4], po[4];
+          float p[4];
           bool seen[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             seen[x] = !MASKED || key0 + 8 * (x >> 1) < lim[nt][x & 1];
-            p[x] = ex2_approx(fmaf(y[u][nt][x], unit[nt][x & 1], -m2[nt][x & 1]));
+            p[x] = ex2_approx(fmaf(y[u][nt][x], a.scale2, -m2[nt][x & 1]));
             if (!seen[x]) p[x] = 0.f;
             l[nt][x & 1] += p[x];
-            po[x] = p[x] * om;
           }
 #pragma unroll
           for (int z = 0; z < NG; ++z) {
             float ps[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const float sc = lo_f(vs[u][x >> 1][z]), ba = F32 ? fmaf(8.f, sc, hi_f(vs[u][x >> 1][z])) : hi_f(vs[u][x >> 1][z]);
-              ps[x] = po[x] * sc;
+              const float sc = lo_f(vs[u][x >> 1][z]), ba = fmaf(8.f, sc, hi_f(vs[u][x >> 1][z]));
+              ps[x] = p[x] * (F32 ? sc : sc * om[z]);
               if constexpr (MASKED) {
                 off[nt][z][x & 1] += seen[x] ? p[x] * ba : 0.f;  // a token that another query sees may be NaN
                 if (!seen[x]) ps[x] = 0.f;
@@ -701,8 +740,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
               }
             }
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-              const uint32_t u0 = pack2(ps[0], ps[1]), u1 = pack2(ps[2], ps[3]);
+            for (int part = 0; part < PP; ++part) {
+              const uint32_t u0 = WIDE ? pack2(ps[0], ps[1]) : pack2_f16(ps[0], ps[1]);
+              const uint32_t u1 = WIDE ? pack2(ps[2], ps[3]) : pack2_f16(ps[2], ps[3]);
               b[nt][z][part][0] = transpose8(u0);
               b[nt][z][part][1] = transpose8(u1);
               rest2(u0, ps[0], ps[1]);
@@ -729,18 +769,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
           const uint32_t xx = __byte_perm(vw[0][h >> 1], vw[1][h >> 1], sel);
           const uint32_t yy = __byte_perm(vw[2][h >> 1], vw[3][h >> 1], sel);
           uint32_t c0[4], c1[4];
-          codes8<F32>(xx, kc, c0);
-          codes8<F32>(yy, kc, c1);
+          codes8<!WIDE>(xx, kc, c0);
+          codes8<!WIDE>(yy, kc, c1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int p = PARTS - 1; p >= 0; --p) {
+            for (int p = PP - 1; p >= 0; --p) {
               const uint32_t b0 = b[nt][h * NG / W][p][0], b1 = b[nt][h * NG / W][p][1];
-              mma(O[nt][2 * h], c0[0], c0[1], c1[0], c1[1], b0, b1);
-              mma(O[nt][2 * h + 1], c0[2], c0[3], c1[2], c1[3], b0, b1);
+              mma<!WIDE>(O[nt][2 * h], c0[0], c0[1], c1[0], c1[1], b0, b1);
+              mma<!WIDE>(O[nt][2 * h + 1], c0[2], c0[3], c1[2], c1[3], b0, b1);
             }
         }
       }
+      return true;
     };
 
     for (int t = sh.t0; t < sh.t1; ++t) {
@@ -749,16 +790,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       const uint8_t* stage = smem + st * S::kStage;
       const int tok = t * kTile + warp * 16;
       // both halves at once where every query sees all of them and the registers allow (16 queries spill, 192 rows of
-      // 6400 keys, g = 16, 82 us against 74; 8 queries with groups of 32, 60.7 against 58; 8 with groups of 64, 49.8 against
-      // 53.5 one after the other)
+      // 6400 keys, g = 16, 82 us against 74 when measured; 8 queries with groups of 32, 60.7 against 58; 8 with groups
+      // of 64, 49.8 against 53.5 one after the other)
       constexpr int U = NT == 1 && (NG < 4 || F32) ? 2 : 1;
-      if (tok + 64 + 16 <= lim_min) {
+      int u0 = 0;
+      bool fast = tok + 64 + 16 <= lim_min && (F32 || !wide);
+      if (fast) {
 #pragma unroll 1
         for (int u = 0; u < 2; u += U)
-          attend(std::integral_constant<int, U>{}, std::false_type{}, stage, u, t);
-      } else {
+          if (!attend(std::integral_constant<int, U>{}, std::false_type{}, stage, u, t)) {
+            fast = false;
+            u0 = u;
+            break;
+          }
+      }
+      if (!fast) {
 #pragma unroll 1
-        for (int u = 0; u < 2 && tok + 64 * u < len; ++u)
+        for (int u = u0; u < 2 && tok + 64 * u < len; ++u)
           attend(std::integral_constant<int, 1>{}, std::true_type{}, stage, u, t);
       }
       __syncwarp();
@@ -770,8 +818,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     }
 
     // ---- the CTA leaves the row: the warps' sums are joined
-    const float inv = 1.f / om;
-    const float ue = F32 ? 1.f : 0x1p24f, uo = F32 ? 1.f : 0x1p20f;  // the codes' units, even and odd channels
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -787,9 +833,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
 #pragma unroll
         for (int h = 0; h < W; ++h) {
           const float add = off[nt][h * NG / W][x];
+          const float inv = om[h * NG / W] > 0.f ? __frcp_rn(om[h * NG / W]) : 0.f;  // 0: the warp had no key
           *reinterpret_cast<float4*>(obuf + (warp * NQ + qi) * S::kORow + 32 * h + 4 * grp) =
-              make_float4(fmaf(O[nt][2 * h][x] * ue, inv, add), fmaf(O[nt][2 * h][2 + x] * uo, inv, add),
-                          fmaf(O[nt][2 * h + 1][x] * ue, inv, add), fmaf(O[nt][2 * h + 1][2 + x] * uo, inv, add));
+              make_float4(fmaf(O[nt][2 * h][x], inv, add), fmaf(O[nt][2 * h][2 + x], inv, add),
+                          fmaf(O[nt][2 * h + 1][x], inv, add), fmaf(O[nt][2 * h + 1][2 + x], inv, add));
         }
         if (grp == 0) ml[warp * NQ + qi] = make_float2(m2[nt][x], l[nt][x]);
       }
@@ -967,6 +1014,7 @@ int launch_paged_attn(const kv_paged_shape& sh, const PageGeom& g, const SeqRows
   a.group = sh.group;
   a.R = n_q * sh.group;
   a.scale2 = 1.4426950408889634f / sqrtf((float)sh.head_dim);
+  a.inv_scale2 = 1.f / a.scale2;
   a.q = q;
   a.out = out;
   a.lse = lse;
@@ -974,7 +1022,7 @@ int launch_paged_attn(const kv_paged_shape& sh, const PageGeom& g, const SeqRows
   a.arrived = reinterpret_cast<int*>(ws + w.arrived);
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.limit_ns = wait_limit_ns();
-  a.kc = {0x64006400u, 0x54005400u, 0xe408e408u, 0xd480d480u};
+  a.kc = {0x43004300u, 0xc308c308u, 0x64006400u, 0x54005400u, 0xe408e408u, 0xd480d480u};
   const bool f32 = sh.dtype == KV_F32;
   if (g.d == 64) return g.G == 1 ? run_as<64, 1>(a, f32, st) : run_as<64, 2>(a, f32, st);
   return g.G == 1 ? run_as<128, 1>(a, f32, st) : g.G == 2 ? run_as<128, 2>(a, f32, st) : run_as<128, 4>(a, f32, st);
