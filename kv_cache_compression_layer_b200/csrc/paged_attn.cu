@@ -261,7 +261,7 @@ __device__ __forceinline__ float lse_of(float M, float L) {
 template <int D, int NG, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2) paged_attn_kernel(const AttnArgs a) {
   using S = Smem<D, NG, NT, F32>;
-  constexpr int W = D / 32, NQ = S::NQ, QP = F32 ? 3 : 1, kStages = S::kStages;
+  constexpr int W = D / 32, NQ = S::NQ, QP = F32 ? 3 : 1, kChain = F32 ? 8 : 32, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   float* obuf = reinterpret_cast<float*>(smem + S::kObuf);
   float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
@@ -532,18 +532,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int x = 0; x < 2 * W; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) O[nt][x][y] = 0.f;
-#pragma unroll
       for (int x = 0; x < NG; ++x) off[nt][x][0] = off[nt][x][1] = 0.f;
       m2[nt][0] = m2[nt][1] = thr[nt][0] = thr[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
     float om[NG];         // the scales of p' and O by group of channels; 0: not yet chosen
     bool wide = F32;      // no scale any more: steps lay too far apart
+    bool moved = false;   // sums lie in the warp's part of obuf
 #pragma unroll
     for (int z = 0; z < NG; ++z) om[z] = F32 ? 1.f : 0.f;
+    // This lane's four channels of part h of a row and query (nt, x) there.
+    auto spot = [&](int nt, int x, int h) {
+      return reinterpret_cast<float4*>(obuf + (warp * NQ + nt * 8 + 2 * tig + x) * S::kORow + 32 * h + 4 * grp);
+    };
+
+
     // The warp's 16 keys of each of the halves u0 .. u0 + U - 1 of tile t in stage st; MASKED: some may be hidden from
     // some query, and steps may lie apart (WIDE). False: not done, since they do.
     auto attend = [&](auto uu, auto mk, const uint8_t* st, int u0, int t) {
@@ -709,6 +712,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
               O[nt][z][x] *= f;
               O[nt][z][2 + x] *= f;
             }
+            if (moved) {
+#pragma unroll
+              for (int h = 0; h < W; ++h) {
+                const float4 v = *spot(nt, x, h);
+                *spot(nt, x, h) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+              }
+            }
           }
       }
 #pragma unroll
@@ -784,37 +794,63 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       return true;
     };
 
-    for (int t = sh.t0; t < sh.t1; ++t) {
-      ok = wait(&full[st], turn & 1);
-      if (!ok) break;
-      const uint8_t* stage = smem + st * S::kStage;
-      const int tok = t * kTile + warp * 16;
-      // both halves at once where every query sees all of them and the registers allow (16 queries spill, 192 rows of
-      // 6400 keys, g = 16, 82 us against 74 when measured; 8 queries with groups of 32, 60.7 against 58; 8 with groups
-      // of 64, 49.8 against 53.5 one after the other)
-      constexpr int U = NT == 1 && (NG < 4 || F32) ? 2 : 1;
-      int u0 = 0;
-      bool fast = tok + 64 + 16 <= lim_min && (F32 || !wide);
-      if (fast) {
+    // The matrix unit cuts a running sum's last bits off, towards zero, at each of two products a tile (fp32: six):
+    // after kChain tiles the sums go to the warp's place in shared memory, where additions round to nearest.
+    for (int t = sh.t0; ok && t < sh.t1;) {
+      const int end = min(sh.t1, t + kChain);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2 * W; ++x)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) O[nt][x][z] = 0.f;
+      for (; t < end; ++t) {
+        ok = wait(&full[st], turn & 1);
+        if (!ok) break;
+        const uint8_t* stage = smem + st * S::kStage;
+        const int tok = t * kTile + warp * 16;
+        // both halves at once where every query sees all of them and the registers allow (16 queries spill, 192 rows of
+        // 6400 keys, g = 16, 82 us against 74 when measured; 8 queries with groups of 32, 60.7 against 58; 8 with groups
+        // of 64, 49.8 against 53.5 one after the other)
+        constexpr int U = NT == 1 && (NG < 4 || F32) ? 2 : 1;
+        int u0 = 0;
+        bool fast = tok + 64 + 16 <= lim_min && (F32 || !wide);
+        if (fast) {
 #pragma unroll 1
-        for (int u = 0; u < 2; u += U)
-          if (!attend(std::integral_constant<int, U>{}, std::false_type{}, stage, u, t)) {
-            fast = false;
-            u0 = u;
-            break;
+          for (int u = 0; u < 2; u += U)
+            if (!attend(std::integral_constant<int, U>{}, std::false_type{}, stage, u, t)) {
+              fast = false;
+              u0 = u;
+              break;
+            }
+        }
+        if (!fast) {
+#pragma unroll 1
+          for (int u = u0; u < 2 && tok + 64 * u < len; ++u)
+            attend(std::integral_constant<int, 1>{}, std::true_type{}, stage, u, t);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+        if (++st == kStages) {
+          st = 0;
+          ++turn;
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int h = 0; h < W; ++h) {
+            const float inv = om[h * NG / W] > 0.f ? __frcp_rn(om[h * NG / W]) : 0.f;  // 0: the warp had no key
+            float4 v = moved ? *spot(nt, x, h) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v.x = fmaf(O[nt][2 * h][x], inv, v.x);
+            v.y = fmaf(O[nt][2 * h][2 + x], inv, v.y);
+            v.z = fmaf(O[nt][2 * h + 1][x], inv, v.z);
+            v.w = fmaf(O[nt][2 * h + 1][2 + x], inv, v.w);
+            *spot(nt, x, h) = v;
           }
-      }
-      if (!fast) {
-#pragma unroll 1
-        for (int u = u0; u < 2 && tok + 64 * u < len; ++u)
-          attend(std::integral_constant<int, 1>{}, std::true_type{}, stage, u, t);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
-      if (++st == kStages) {
-        st = 0;
-        ++turn;
-      }
+      moved = true;
     }
 
     // ---- the CTA leaves the row: the warps' sums are joined
@@ -833,10 +869,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
 #pragma unroll
         for (int h = 0; h < W; ++h) {
           const float add = off[nt][h * NG / W][x];
-          const float inv = om[h * NG / W] > 0.f ? __frcp_rn(om[h * NG / W]) : 0.f;  // 0: the warp had no key
-          *reinterpret_cast<float4*>(obuf + (warp * NQ + qi) * S::kORow + 32 * h + 4 * grp) =
-              make_float4(fmaf(O[nt][2 * h][x], inv, add), fmaf(O[nt][2 * h][2 + x], inv, add),
-                          fmaf(O[nt][2 * h + 1][x], inv, add), fmaf(O[nt][2 * h + 1][2 + x], inv, add));
+          const float4 v = *spot(nt, x, h);
+          *spot(nt, x, h) = make_float4(v.x + add, v.y + add, v.z + add, v.w + add);
         }
         if (grp == 0) ml[warp * NQ + qi] = make_float2(m2[nt][x], l[nt][x]);
       }

@@ -1,6 +1,7 @@
-"""kv_paged_attn keeps its sums in float32: rows whose channel groups or tokens
-lie many powers of two apart, where a scale shared between them would cost the
-small ones their bits. Against float64 over the values held, within bounds that
+"""kv_paged_attn keeps its sums in float32: long even rows, where what each
+addition loses could pile up on one side, and rows whose channel groups or
+tokens lie many powers of two apart, where a scale shared between them would
+cost the small ones their bits. Against float64 over the values held, within bounds that
 count float32 roundings, the output's, and for bf16 that of weights to fp16."""
 import math
 
@@ -13,6 +14,8 @@ from tests import _paged as pg
 
 pytestmark = pytest.mark.gpu
 
+CHAIN = 64  # products that are added up in the matrix unit, at most, before the sum leaves it
+
 
 def strict(m, q, row, n_q=1):
     """out, lse and bounds of their errors for q [n_q * g, d] (float64) of a row.
@@ -21,8 +24,9 @@ def strict(m, q, row, n_q=1):
     times the sum of its channels, round in float32, relative to the terms of their own group: a logit of key j is off
     by at most E_j = (d + 16) 2^-23 sum_c |q_c| (16 s_jc + |m_jc|) / sqrt d. A weight p_j is off by a factor within
     2 E + 2^-20 (exp2, the sum). Output: a channel's terms are p_j (16 s_jc + |m_jc|); their sums round 2^-23 of the
-    sum of magnitudes W_c for each of the n / 64 products of a warp that follow each other, 2^-24 of it for each of a
-    lane's n / 32 additions of bases, and 16 and one for each tile more where sums are rescaled and joined. A bf16 call rounds weights times steps to fp16: 2^-11 of them
+    sum of magnitudes W_c for each of a warp's products that follow each other (n / 64, CHAIN at most) and for each of
+    the sums of CHAIN of them, 2^-24 of it for each of a lane's n / 32 additions of bases, and 16 and one for each tile
+    more where sums are rescaled and joined. A bf16 call rounds weights times steps to fp16: 2^-11 of them
     times |c - 8| <= 8 steps, 2^-12 of the terms, and 2^-22 of the largest weight's step or more, 8 times, for each key
     (or to two bf16, less than that). A weight below 2^-126 may be lost: 2^-118 of the largest term for each key
     (weights are below 2^8 and the largest is 1 or more)."""
@@ -44,7 +48,7 @@ def strict(m, q, row, n_q=1):
         rel = 2 * E + 2.0 ** -20
         mag = 16 * v[:, 1] + np.abs(v[:, 2])
         W = p @ mag / z
-        c = (n / 64 + 17 + n / 128) * 2.0 ** -23 + n / 32 * 2.0 ** -24
+        c = (min(CHAIN, n / 64 + 1) + n / 64 / CHAIN + 16 + n / 128) * 2.0 ** -23 + n / 32 * 2.0 ** -24
         c += 0 if f32 else 2.0 ** -12
         tol[i] = (p * rel) @ mag / z + (p @ rel / z) * np.abs(out[i]) + c * W + n * 2.0 ** -118 * mag.max(0)
         tol[i] += 0 if f32 else n * 2.0 ** -19 * (p[:, None] * v[:, 1]).max(0) / z
@@ -60,6 +64,72 @@ def check(m, q, out, lse, seqs, n_q=1):
         err = np.abs(O[i].reshape(o.shape) - o)
         assert (err <= tol).all(), (i, float((err / tol).max()), np.unravel_index((err / tol).argmax(), err.shape))
         assert (np.abs(Z[i].reshape(-1) - z) <= tol_z).all(), i
+
+
+@pytest.mark.parametrize("spread", ["even", "one_sided"])
+@pytest.mark.parametrize("g", [1, 16])
+@pytest.mark.parametrize("dtype", [kv.KV_BF16, kv.KV_F32])
+def test_long_even_rows(dtype, g, spread):
+    """896 rows of 32768 keys, whole rows in one block, with next to the same weight for each key: outputs are means
+    of many values that cancel, so what sums lose would show. one_sided: a channel far below the others puts their
+    codes next to 15, so that sums of codes grow all along the row.
+
+    Queries have one channel, so a weight is off by a factor within rel = 2 (d + 16) 2^-23 |q| (16 s + |m|) / sqrt d +
+    2^-20 with that channel's s and m. A sum of CHAIN products of 16 keys each loses 2^-23 of what it has reached at
+    each, CHAIN / 2 2^-23 of 8 s a key on average; sums of those and of bases (a lane adds n / 32) as in strict().
+
+    The mean over all outputs of the error: the matrix unit cuts a sum's last bits off, to one side, 2^-24 of what it has
+    reached on average (its last place is 2^-23 to 2^-24 of it); all else is rounded to the nearest and has no sign: 8 /
+    sqrt(count) of the bounds above."""
+    rng = np.random.default_rng(23)
+    n, R, d = 32768, 896, 128
+    base, m = pg.make(n_seqs=1, n_layers=1, heads=8, group=1, dtype=dtype, max_pages=512)
+    K, V = pg.tokens(rng, 8 * n, d, dtype)
+    if spread == "one_sided":
+        V[:, [5, 77]] = -10.0
+    rows = m.call_rows([0])
+    K, V = K.reshape(8, n, d), V.reshape(8, n, d)
+    m.append(rows, K, V)
+    base.append([0], pg.up(K, dtype, base.device), pg.up(V, dtype, base.device))
+    pages = torch.randint(0, 4096, (R, n // 64), generator=torch.Generator().manual_seed(1)).to(base.device)
+    sh = kv.make_paged_shape(64, 1, 14, g, d, dtype, 4096, n // 64, 64, 64)
+    cache = kv.PagedCache(sh, pages=base.pages, table=pages.to(torch.int32),
+                          lens=torch.full((R,), n, dtype=torch.int32, device=base.device))
+    q = torch.zeros(R, g, d, dtype=pg.DT[dtype], device=base.device)
+    q[:, :, 9] = 0.05 * (1 + torch.rand(R, g, generator=torch.Generator().manual_seed(2))).to(q)
+    lse = torch.empty(R, g, device=base.device)
+    out = cache.attend(list(range(64)), q, lse=lse).double()
+    # by page number: the keys' channel 9, values, steps and centres
+    k9, val = (torch.zeros(4096, 64, *x, dtype=torch.float64, device=base.device) for x in ((), (d,)))
+    s, mid = (torch.zeros(4096, d, dtype=torch.float64, device=base.device) for _ in range(2))
+    e9 = 0.0
+    up = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(base.device)  # noqa: E731
+    for r in rows:
+        at = up(np.asarray(m.lists[r]))
+        x = m.V[r].reshape(n // 64, 64, 3, d)
+        k9[at], val[at] = up(m.K[r].reshape(n // 64, 64, 3, d)[:, :, 0, 9]), up(x[:, :, 0])
+        s[at], mid[at] = up(x[:, :, 1].sum(1)), up(np.abs(x[:, :, 2] + 8 * x[:, :, 1]).sum(1))
+        e9 = max(e9, (16 * m.K[r][:, 1, 9] + np.abs(m.K[r][:, 2, 9])).max())
+    rel = 2 * (d + 16) * 2.0 ** -23 * 0.1 * e9 / math.sqrt(d) + 2.0 ** -20
+    half = 2.0 ** -24 if dtype == kv.KV_F32 else 2.0 ** -8
+    short = 0.0 if dtype == kv.KV_F32 else 2.0 ** -12
+    err, room, free, cut = [], [], [], []
+    for r in range(R):
+        x = (q[r, :, 9].double()[:, None] * k9[pages[r]].flatten()) / math.sqrt(d)
+        want = torch.softmax(x, 1) @ val[pages[r]].flatten(0, 1)
+        a, b = s[pages[r]].sum(0) / n, mid[pages[r]].sum(0) / n
+        spare = 1.02 * ((CHAIN / 2 + n / 64 / CHAIN + 16) * 2.0 ** -23 * 8 * a + (n / 64 + 16) * 2.0 ** -24 * b
+                        + rel * (8 * a + b))  # weights are within 2 % of each other
+        err.append(out[r] - want)
+        free.append(short * 16 * a + half * want.abs())
+        room.append(spare.expand_as(want))
+        cut.append(((CHAIN / 2 + 8) * 2.0 ** -24 * 8 * a).expand_as(want))
+        assert (lse[r].double() - torch.logsumexp(x, 1)).abs().max() <= rel + 2.0 ** -20 + 2.0 ** -22 * 11
+    err, room, free, cut = (torch.stack(x) for x in (err, room, free, cut))
+    worst = (err.abs() / (room + free * (1 + half) + half * room)).max()
+    assert worst <= 1, float(worst)
+    mean, may = err.mean().abs(), (cut + 8 / math.sqrt(R * d) * (room + free)).mean()
+    assert mean <= may, (float(mean), float(may))
 
 
 def spread_rows(rng, n, d, qg, power):
