@@ -61,6 +61,7 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kRowCost = 2;   // of starting and leaving a row, in tiles
 constexpr int kMinShare = 2;  // cost of a CTA's share, at least
 constexpr int kJoin = 8;      // partials joined at once
+constexpr int kJoined = 1, kLost = 2;  // see last_of
 // Steps times their scale that fp16 p' allow: weights are below 2^8, so p' stays below 2^15; the largest weight so far is 1
 // or more, so its p' is 2^-3 or more, 2^22 times what rounding to the smallest fp16 takes from another.
 constexpr float kReachLo = 0x1p-3f, kReachHi = 0x1p7f;
@@ -474,19 +475,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     const int c_first = whole ? cta : shares.holder(base[r] + kRowCost);
     const int c_count = whole ? 1 : shares.holder(base[r + 1] - 1) - c_first + 1;
     // Counts this CTA's partial of a shared row. The row's CTAs come in eights; `first`, the slot of an eight's first
-    // partial, has the eight's counter, the row counts the eights that are complete. True for the last of n.
+    // partial, has the eight's counter, the row counts the eights that are complete. 0 but for the last of n, for which
+    // it is kJoined, or kLost where one had `lost` its partial (counted in the upper half): then nothing is joined.
     int* arrived = a.arrived + chunk * (2 * gridDim.x + kAttnRows);
-    auto last_of = [&](int* counter, int n) {
-      const bool last = atomicAdd(counter, 1) == n - 1;
-      if (last) *counter = 0;
-      return last;
+    auto last_of = [&](int* counter, int n, bool lost) {
+      const int add = lost ? 0x10001 : 1, now = atomicAdd(counter, add) + add;
+      if ((now & 0xffff) != n) return 0;
+      *counter = 0;
+      return now > 0xffff ? kLost : kJoined;
     };
     const int c_own = cta - c_first, eight = c_own / kJoin;
     const int eights = (c_count + kJoin - 1) / kJoin, in_eight = min(kJoin, c_count - eight * kJoin);
     const int first = eight == 0 ? 2 * c_first + 1 : 2 * (c_first + eight * kJoin);
-    if (!ok) {  // a wait ran out: the counters of the CTA's other rows stay in step all the same
-      if (!whole && threadIdx.x == 0 && last_of(arrived + first, in_eight) && eights > 1)
-        last_of(arrived + 2 * gridDim.x + r, eights);
+    auto give_up_row = [&] {  // a wait ran out: the row's counters stay in step all the same
+      if (!whole && threadIdx.x == 0 && last_of(arrived + first, in_eight, true) && eights > 1)
+        last_of(arrived + 2 * gridDim.x + r, eights, true);
+    };
+    if (!ok) {
+      give_up_row();
       continue;
     }
     ok = wait(&q_full[k & 1], (k >> 1) & 1);
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     // query fragments and their sums by group
     uint32_t qf[NT][QP][W][4];
     float qsum[NT][NG][2];
-    {
+    {  // (where the wait ran out, of what lies there: it meets no key, and the row's output stays)
       const uint4* frag = reinterpret_cast<const uint4*>(smem + S::kQ + (k & 1) * S::kQBytes);
       const float* meta = reinterpret_cast<const float*>(smem + S::kQ + (k & 1) * S::kQBytes + S::kFrag);
 #pragma unroll
@@ -877,8 +883,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
     }
     ok = named_bar_and(1, kWarps * 32, ok);
     if (!ok) {
-      if (!whole && threadIdx.x == 0 && last_of(arrived + first, in_eight) && eights > 1)
-        last_of(arrived + 2 * gridDim.x + r, eights);
+      give_up_row();
       continue;
     }
     constexpr size_t kPart = kAttnQ * (D + 2);  // floats: (max, sum) and the output of up to kAttnQ query rows
@@ -971,20 +976,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         if ((int)threadIdx.x < nq) reinterpret_cast<float2*>(parts + (size_t)s0 * kPart)[threadIdx.x] = ml[threadIdx.x];
       }
     };
-    // whether this CTA is the last of n, for all threads; what they wrote before is seen by who is
+    // last_of for all threads; what they wrote before is seen by who is the last
     auto leave = [&](int* counter, int n) {
       named_bar_sync(1, kWarps * 32);
       if (threadIdx.x == 0) {
         __threadfence();  // what the barrier ordered before it is seen before the count
-        *last_flag = last_of(counter, n);
+        *last_flag = last_of(counter, n, false);
         __threadfence();
       }
       named_bar_sync(1, kWarps * 32);
-      return *last_flag != 0;
+      return *last_flag;
     };
-    if (!leave(arrived + first, in_eight)) continue;
+    const int whose = leave(arrived + first, in_eight);
+    if (whose == kLost && eights > 1 && threadIdx.x == 0) last_of(arrived + 2 * gridDim.x + r, eights, true);
+    if (whose != kJoined) continue;
     join(in_eight, first, 2 * (c_first + eight * kJoin + 1), 2, eights == 1);
-    if (eights == 1 || !leave(arrived + 2 * gridDim.x + r, eights)) continue;
+    if (eights == 1 || leave(arrived + 2 * gridDim.x + r, eights) != kJoined) continue;
     join(eights, 2 * c_first + 1, 2 * (c_first + kJoin), 2 * kJoin, true);
   }
 }
