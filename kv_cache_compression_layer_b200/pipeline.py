@@ -24,7 +24,11 @@ def torch_dtype(dtype_code: int):
 
 
 class Compressor:
-    """All buffers of one batch (shape, audio lengths L per sequence, parameters)."""
+    """All buffers of one batch (shape, audio lengths L per sequence, parameters).
+
+    ``b``, ``slot_off`` and ``pos`` are the lists of the latest call that made some: those of the
+    decode cache (``allocate``, ``compress``), or those of the pages (``compress_paged``).
+    """
 
     def __init__(self, shape: kv_shape, L: Sequence[int], params: kv_params, device="cuda"):
         self.shape, self.L, self.params = shape, [int(x) for x in L], params
@@ -46,9 +50,10 @@ class Compressor:
         self.s = torch.empty(self.n_keys, dtype=f32, device=dev)
         self.s_hat = torch.empty(self.n_keys, dtype=f32, device=dev)
         self.kstar = torch.empty(self.rows, dtype=i32, device=dev)
-        self.b = torch.empty(self.rows, dtype=i32, device=dev)
-        self.slot_off = torch.empty(self.rows + 1, dtype=torch.int64, device=dev)
-        self.pos = torch.zeros(self.n_slots, dtype=i32, device=dev)
+        self._decode_lists, self._paged_lists = (
+            (torch.empty(self.rows, dtype=i32, device=dev), torch.empty(self.rows + 1, dtype=torch.int64, device=dev),
+             torch.zeros(self.n_slots, dtype=i32, device=dev)) for _ in range(2))
+        self.b, self.slot_off, self.pos = self._decode_lists
         self.Kc = torch.zeros(self.n_slots, d, dtype=dt, device=dev)
         self.Vc = torch.zeros(self.n_slots, d, dtype=dt, device=dev)
         self.A = torch.zeros(self.n_slots, dtype=f32, device=dev)
@@ -61,6 +66,7 @@ class Compressor:
 
     # -- prefill compression -------------------------------------------------
     def allocate(self, S: torch.Tensor, stream=None):
+        self.b, self.slot_off, self.pos = self._decode_lists
         kv_allocate(self.shape, self.L, self.params, S, self.b, self.slot_off, stream)
 
     def score(self, qwin: torch.Tensor, K: torch.Tensor, stream=None):
@@ -70,6 +76,7 @@ class Compressor:
         kv_sss(self.shape, self.L, self.s, self.s_hat, self.kstar, self.params.alpha, self.params.rho, stream)
 
     def select_gather(self, K: torch.Tensor, V: torch.Tensor, stream=None):
+        self.b, self.slot_off, self.pos = self._decode_lists
         kv_select_gather(self.shape, self.L, self.s_hat, K, V, self.b, self.slot_off, self.pos, self.Kc, self.Vc,
                          stream)
 
@@ -90,14 +97,15 @@ class Compressor:
                        spikes: Optional[torch.Tensor] = None, stream=None):
         """allocate -> score -> (harness spikes) -> SSS -> select, then the kept tokens of the batch's
         sequence i, quantised, behind those of sequence seqs[i] of ``cache`` (kv_paged_append; no
-        compacted copy is written, and the decode cache of this object is not touched but for
-        ``pos``, which holds the kept positions)."""
+        compacted copy is written). The kept lists are left in ``b``, ``slot_off`` and ``pos``; the
+        decode cache of this object keeps its own and may go on."""
         sh, cs = self.shape, cache.shape
         if (cs.n_layers, cs.n_kv_heads, cs.head_dim, cs.dtype) != (sh.n_layers, sh.n_kv_heads, sh.head_dim, sh.dtype):
             raise ValueError("the cache holds rows of another shape")
         if len(seqs) != len(self.L):
             raise ValueError(f"{len(self.L)} sequences, got {len(seqs)}")
-        self.allocate(S, stream)
+        self.b, self.slot_off, self.pos = self._paged_lists
+        kv_allocate(self.shape, self.L, self.params, S, self.b, self.slot_off, stream)
         self.score(qwin, K, stream)
         if spikes is not None:
             self.s.mul_(spikes)

@@ -1,0 +1,52 @@
+"""Compressor.compress_paged beside the rest of a Compressor's work."""
+import numpy as np
+import pytest
+import torch
+
+import kv_cache_compression_layer_b200 as kv
+import synth
+from tests._harness import dev, up
+from tests.test_gpu_paged_pipeline import make
+
+pytestmark = pytest.mark.gpu
+
+
+def inputs(cfg, bt, dt):
+    return up(bt.qwin, dt), up(bt.K, dt), up(bt.V, dt), up(bt.S, torch.float32)
+
+
+@pytest.mark.parametrize("name", ["ragged", "tiny"])
+def test_decoding_goes_on(name):
+    """Decode steps before and after the batch is compressed into pages, with other relevances, are those of a
+    Compressor that does nothing else; the pages get their own lists."""
+    cfg = synth.small(name, n_layers=2, L=(700, 1500, 1000)) if name != "tiny" else synth.CONFIGS["tiny"].with_(n_layers=2)
+    dt, code = (torch.bfloat16, kv.KV_BF16) if name != "tiny" else (torch.float32, kv.KV_F32)
+    steps, n = 8, len(cfg.L)
+    bt = synth.make_batch(cfg, steps=steps)
+    comp, cache, _ = make(cfg, code, n)
+    twin, _, _ = make(cfg, code, n)
+    qwin, K, V, S = inputs(cfg, bt, dt)
+    S2 = S.flip(-1) * torch.linspace(0.2, 3.0, S.numel(), device=S.device).view_as(S)
+    comp.compress(qwin, K, V, S)
+    twin.compress(qwin, K, V, S)
+    assert torch.equal(comp.pos, twin.pos)
+    for t in range(steps):
+        if t == 4:
+            comp.compress_paged(cache, list(range(n)), qwin, K, V, S2)
+            other, _, _ = make(cfg, code, n)
+            other.compress(qwin, K, V, S2)
+            assert not torch.equal(other.b, twin.b) and torch.equal(comp.b, other.b)
+            assert torch.equal(comp.slot_off, other.slot_off)
+            for (b, pos, _, _), (b2, pos2, _, _) in zip(comp.kept(), other.kept()):
+                assert b == b2 and np.array_equal(pos, pos2)
+            assert torch.equal(cache.lens, other.b) and cache.read_status() == 0
+        outs = []
+        for c in (comp, twin):
+            out = torch.empty(cfg.rows, cfg.group, cfg.head_dim, dtype=dt, device=dev())
+            c.decode_step(up(bt.q_dec[t], dt), up(bt.k_dec[t], dt), up(bt.v_dec[t], dt), out)
+            outs.append(out)
+        assert torch.equal(outs[0], outs[1]), t
+        assert int(comp.status[0]) == 0 and int(twin.status[0]) == 0
+    comp.compress(qwin, K, V, S2)
+    for x, y in zip(comp.kept(), other.kept()):  # (spare slots keep what decoding left there)
+        assert x[0] == y[0] and all(np.array_equal(a, b) for a, b in zip(x[1:], y[1:]))
