@@ -20,6 +20,14 @@ from . import (KV_BF16, KV_MAX_SEQ, kv_paged_append, kv_paged_attn, kv_paged_com
                kv_read_device_status, make_paged_cache)
 
 
+def on_stream(stream, device):
+    """A context in which torch works on ``stream``: a torch stream, or a raw one's address (0: the default stream)."""
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
 class PagedCache:
     """One cache: a pool of pages, the rows' page lists and lengths, and a workspace.
 
@@ -79,12 +87,7 @@ class PagedCache:
         return torch.cuda.device(self.device)
 
     def _on(self, stream):
-        if stream is None:
-            return self._here()
-        if isinstance(stream, int):
-            stream = (torch.cuda.ExternalStream(stream, device=self.device) if stream
-                      else torch.cuda.default_stream(self.device))
-        return torch.cuda.stream(stream)
+        return self._here() if stream is None else on_stream(stream, self.device)
 
     def _is(self, name: str, x: torch.Tensor, dtype, numel: int, at_least: bool = False):
         if x.dtype != dtype or x.device != self.device or not x.is_contiguous():

@@ -9,6 +9,7 @@ straight from K and V.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from typing import Optional, Sequence
 
 import torch
@@ -16,7 +17,7 @@ import torch
 from . import (KV_BF16, META_INTS, kv_allocate, kv_decode_attn_update, kv_decode_init, kv_decode_scratch_bytes,
                kv_params, kv_score, kv_select, kv_select_gather, kv_shape, kv_sss, kv_total_slots, kv_workspace_bytes,
                make_cache)
-from .paged import PagedCache
+from .paged import PagedCache, on_stream
 
 
 def torch_dtype(dtype_code: int):
@@ -72,6 +73,12 @@ class Compressor:
     def score(self, qwin: torch.Tensor, K: torch.Tensor, stream=None):
         kv_score(self.shape, self.L, qwin, K, self.s, self.ws, self.ws_bytes, stream)
 
+    def _spike(self, spikes: Optional[torch.Tensor], stream):
+        """The harness's spikes on the scores, in the call's stream."""
+        if spikes is not None:
+            with nullcontext() if stream is None else on_stream(stream, self.device):
+                self.s.mul_(spikes)
+
     def sss(self, stream=None):
         kv_sss(self.shape, self.L, self.s, self.s_hat, self.kstar, self.params.alpha, self.params.rho, stream)
 
@@ -87,8 +94,7 @@ class Compressor:
         """allocate -> score -> (harness spikes) -> SSS -> select + gather -> decode init."""
         self.allocate(S, stream)
         self.score(qwin, K, stream)
-        if spikes is not None:
-            self.s.mul_(spikes)
+        self._spike(spikes, stream)
         self.sss(stream)
         self.select_gather(K, V, stream)
         self.decode_init(stream)
@@ -107,8 +113,7 @@ class Compressor:
         self.b, self.slot_off, self.pos = self._paged_lists
         kv_allocate(self.shape, self.L, self.params, S, self.b, self.slot_off, stream)
         self.score(qwin, K, stream)
-        if spikes is not None:
-            self.s.mul_(spikes)
+        self._spike(spikes, stream)
         self.sss(stream)
         kv_select(self.shape, self.L, self.s_hat, self.b, self.slot_off, self.pos, stream)
         cache.append(seqs, K, V, count=self.b, src_off=self.key_off, idx=self.pos, idx_off=self.slot_off,

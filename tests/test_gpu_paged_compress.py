@@ -50,3 +50,43 @@ def test_decoding_goes_on(name):
     comp.compress(qwin, K, V, S2)
     for x, y in zip(comp.kept(), other.kept()):  # (spare slots keep what decoding left there)
         assert x[0] == y[0] and all(np.array_equal(a, b) for a, b in zip(x[1:], y[1:]))
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("as_int", [False, True])
+def test_spikes_on_the_stream_that_is_given(paged, as_int):
+    """Spikes multiply the scores between scoring and smoothing on the call's stream, whatever the current one does."""
+    cfg = synth.small("ragged", n_layers=2, L=(700, 1500))
+    bt = synth.make_batch(cfg, steps=1)
+    qwin, K, V, S = inputs(cfg, bt, torch.bfloat16)
+    comp, cache, _ = make(cfg, kv.KV_BF16, 4)
+    spikes = torch.ones(comp.n_keys, device=dev())
+    spikes[::7] = 300.0
+
+    def run(seqs, spikes, stream=None):
+        if paged:
+            comp.compress_paged(cache, seqs, qwin, K, V, S, spikes=spikes, stream=stream)
+        else:
+            comp.compress(qwin, K, V, S, spikes=spikes, stream=stream)
+
+    def kept():
+        torch.cuda.synchronize()
+        return [(b, pos.copy()) for b, pos, _, _ in comp.kept()]
+
+    def same(x, y):
+        return all(b == c and np.array_equal(p, r) for (b, p), (c, r) in zip(x, y))
+
+    run([0, 1], None)
+    without = kept()
+    cache.free([0, 1])
+    run([0, 1], spikes)
+    want = kept()
+    assert not same(want, without)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms of the current stream
+    run([2, 3], spikes, st.cuda_stream if as_int else st)
+    assert same(kept(), want)
+    if paged:
+        q = torch.randn(cfg.rows, cfg.group, cfg.head_dim, device=dev()).to(torch.bfloat16)
+        assert torch.equal(cache.attend([0, 1], q), cache.attend([2, 3], q)) and cache.read_status() == 0
