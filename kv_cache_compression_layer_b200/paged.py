@@ -140,6 +140,9 @@ class PagedCache:
                     raise ValueError("idx goes with idx_off")
                 self._is("idx", idx, torch.int32, idx.numel())
                 self._is("idx_off", idx_off, torch.int64, n, at_least=True)
+                if idx.numel() == 0:  # an empty tensor has no address, which would mean "without idx":
+                    idx = idx_off = None  # no token has a source
+                    n_src = 0
         if count is None and n_src == 0:
             return
         with self._here():
