@@ -209,8 +209,11 @@ class PagedCache:
         self._is("idx", idx, torch.int32, idx.numel())
         self._is("idx_off", idx_off, torch.int64, n, at_least=True)
         self._is("count", count, torch.int32, n)
-        if idx.numel() == 0:
-            idx = count  # nothing is kept and idx not read, but an empty tensor has no address
+        if idx.numel() == 0:  # no list: a token that is asked for all the same has a position that no row has
+            with self._on(stream):
+                idx = torch.full((self.shape.max_pages * self.shape.page_tokens,), -1, dtype=torch.int32,
+                                 device=self.device)
+                idx_off = torch.zeros(n, dtype=torch.int64, device=self.device)
         with self._here():
             kv_paged_compact(self.shape, self.cache, src, dst, idx, idx_off, count, stream)
 

@@ -37,3 +37,30 @@ def test_append_by_an_empty_list(dtype):
     m.append(m.call_rows([0, 1]), zeros, zeros)
     m.status |= kv.KV_DEV_RANGE
     m.check(cache)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compact_by_an_empty_list(in_place):
+    """No position exists: the tokens asked for are zeros and KV_DEV_RANGE is set; more than a row holds is refused."""
+    rng = np.random.default_rng(1)
+    cache, m = filled(rng)
+    dev = cache.device
+    none = torch.empty(0, dtype=torch.int32, device=dev)
+    off = torch.tensor([0, 0, 1 << 40], device=dev)  # of a list that has no entry
+    dst = [0] if in_place else [2]
+    for stream in (None, torch.cuda.Stream()):
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        cache.compact([0], dst, none, off, torch.tensor([20, 3], dtype=torch.int32, device=dev), stream=stream)
+        m.compact([0], dst, [[-1] * 20, [-1] * 3])
+        m.check(cache)
+        if not in_place:
+            cache.free([2])
+            m.free([2])
+    cache.compact([0], dst, none, off, torch.tensor([257, 0], dtype=torch.int32, device=dev))
+    m.compact([0], dst, [[-1] * 257, []])
+    assert m.status == kv.KV_DEV_RANGE | kv.KV_DEV_CAPACITY
+    m.check(cache)
+    cache.compact([1], [1], none, off, torch.zeros(2, dtype=torch.int32, device=dev))
+    m.compact([1], [1], [[], []])
+    m.check(cache)
