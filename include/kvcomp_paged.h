@@ -117,6 +117,8 @@ int kv_paged_rebuild(const kv_paged_shape* shape, const kv_paged_cache* cache, v
  *   idx     : device int32, or NULL. Token t of call row i is source row
  *             src_off[i] + idx[idx_off[i] + t], without idx src_off[i] + t.
  *   idx_off : device int64 [call rows] (more entries are not read), with idx.
+ *   idx holds every entry that a row's idx_off and count reach; the call cannot
+ *   check that. Lists are aligned to their type (KV_ERR_ARG).
  *   With count = b, idx and idx_off = slot_off of kv_select_gather (or of
  *   kv_select) and src_off = the rows' key offsets this stores the kept tokens
  *   of a batch without the compacted copy in between.
@@ -200,6 +202,8 @@ int kv_paged_copy(const kv_paged_shape* src_shape, const kv_paged_cache* src_cac
  *             that is not below it is stored as zeros, KV_DEV_RANGE).
  *   idx_off : device int64 [n * n_layers * n_kv_heads] (more are not read).
  *   count   : device int32 [n * n_layers * n_kv_heads]; a negative count is 0.
+ *   As for kv_paged_append, idx holds every entry that is reached, and lists are
+ *   aligned to their type.
  * A row whose list would pass max_pages is left as it was (KV_DEV_CAPACITY).
  * Errors: KV_ERR_ARG, KV_ERR_WORKSPACE, KV_ERR_CUDA.
  */

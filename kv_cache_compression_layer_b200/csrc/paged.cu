@@ -1070,6 +1070,10 @@ __global__ void __launch_bounds__(kRowThreads) paged_bits_kernel(int n_pages, co
 
 // ------------------------------------------------------------------- host
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+template <class T>
+bool list_ok(const T* p) {  // aligned to its type, or none
+  return (reinterpret_cast<uintptr_t>(p) & (sizeof(T) - 1)) == 0;
+}
 
 bool cache_ok(const kv_paged_cache* c) {
   return c && aligned16(c->pages) && aligned16(c->table) && aligned16(c->len) && aligned16(c->ref) &&
@@ -1217,6 +1221,7 @@ int kv_paged_append(const kv_paged_shape* shape, const kv_paged_cache* cache, co
   if (n_src < 0 || n_each < 0 || (n_src > 0 && (!aligned16(K) || !aligned16(V)))) return KV_ERR_ARG;
   if (count && !src_off) return KV_ERR_ARG;
   if (idx && (!src_off || !idx_off)) return KV_ERR_ARG;
+  if (!list_ok(count) || !list_ok(src_off) || !list_ok(idx) || !list_ok(idx_off)) return KV_ERR_ARG;
   if (!ws_ok(*shape, *cache)) return KV_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const Ws w = ws_of(*shape, cache->ws);
@@ -1246,7 +1251,7 @@ int kv_paged_load(const kv_paged_shape* shape, const kv_paged_cache* cache, cons
   if (!paged_shape_ok(shape) || !cache_ok(cache)) return KV_ERR_ARG;
   LoadArgs a = {};
   if (!make_rows(*shape, seq, n_seq, layer0, n_lay, true, &a.rows)) return KV_ERR_ARG;
-  if (!out_off || (reinterpret_cast<uintptr_t>(out_off) & 7) || n_out < 0 || !aligned16(K_out) || !aligned16(V_out))
+  if (!out_off || !list_ok(out_off) || n_out < 0 || !aligned16(K_out) || !aligned16(V_out))
     return KV_ERR_ARG;
   if (!ws_ok(*shape, *cache)) return KV_ERR_WORKSPACE;
   a.g = page_geom(*shape);
@@ -1271,7 +1276,7 @@ int kv_paged_attn(const kv_paged_shape* shape, const kv_paged_cache* cache, cons
   if (!make_rows(*shape, seq, n_seq, layer0, n_lay, true, &rows)) return KV_ERR_ARG;
   if (n_q < 1 || n_q > KV_PAGED_MAX_QUERIES || n_q * shape->group > KV_PAGED_MAX_QUERIES) return KV_ERR_ARG;
   if (!aligned16(q) || !aligned16(out) || q == out) return KV_ERR_ARG;
-  if (lse && (reinterpret_cast<uintptr_t>(lse) & 3)) return KV_ERR_ARG;
+  if (!list_ok(lse)) return KV_ERR_ARG;
   if (!ws_ok(*shape, *cache)) return KV_ERR_WORKSPACE;
   return launch_paged_attn(*shape, page_geom(*shape), rows, cache_of(*cache), static_cast<uint8_t*>(cache->ws), n_q, q,
                            out, lse, static_cast<cudaStream_t>(stream));
@@ -1358,7 +1363,7 @@ int kv_paged_compact(const kv_paged_shape* shape, const kv_paged_cache* cache, c
   if (!make_rows(*shape, src, n, 0, shape->n_layers, false, &p.src) ||
       !make_rows(*shape, dst, n, 0, shape->n_layers, true, &p.dst) || !lists_ok(src, dst, n, true, true))
     return KV_ERR_ARG;
-  if (!idx || !idx_off || !count) return KV_ERR_ARG;
+  if (!idx || !idx_off || !count || !list_ok(idx) || !list_ok(idx_off) || !list_ok(count)) return KV_ERR_ARG;
   if (!ws_ok(*shape, *cache)) return KV_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const Ws w = ws_of(*shape, cache->ws);
