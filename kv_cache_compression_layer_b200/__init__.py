@@ -170,8 +170,9 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
 
-        # torch.cuda.current_stream().cuda_stream without the Stream object (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # torch.cuda.current_stream().cuda_stream without the Stream object (3 us a call), where torch still has that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
