@@ -90,3 +90,47 @@ def test_spikes_on_the_stream_that_is_given(paged, as_int):
     if paged:
         q = torch.randn(cfg.rows, cfg.group, cfg.head_dim, device=dev()).to(torch.bfloat16)
         assert torch.equal(cache.attend([0, 1], q), cache.attend([2, 3], q)) and cache.read_status() == 0
+
+
+def test_a_whole_audio_compacted_by_the_selection():
+    """An audio held in full, then cut in place by kv_select's lists (idx, slot_off and b as they are): the same
+    values as its kept tokens stored straight away. Rows that a call shortens to nothing, or not at all."""
+    cfg = synth.small("3b", n_layers=2, L=(1500,))
+    bt = synth.make_batch(cfg, steps=1)
+    qwin, K, V, S = inputs(cfg, bt, torch.bfloat16)
+    comp, cache, _ = make(cfg, kv.KV_BF16, 3)  # the new pages have to be free beside the old
+    cache.append([0], K.view(cfg.rows, 1500, -1), V.view(cfg.rows, 1500, -1))
+    comp.compress_paged(cache, [1], qwin, K, V, S)
+    assert int(comp.b.max()) < 1500
+    cache.compact([0], [0], comp.pos, comp.slot_off, comp.b)
+    assert cache.read_status() == 0 and torch.equal(cache.lens[:cfg.rows], cache.lens[cfg.rows:2 * cfg.rows])
+    out = [torch.zeros(2, comp.n_slots, cfg.head_dim, dtype=torch.bfloat16, device=dev()) for _ in range(2)]
+    for seq, (k, v) in enumerate(out):
+        cache.load([seq], k, v, comp.slot_off)
+    assert torch.equal(out[0], out[1]) and bool((out[0] != 0).any())
+    q = torch.randn(cfg.rows, cfg.group, cfg.head_dim, device=dev()).to(torch.bfloat16)
+    assert torch.equal(cache.attend([0], q), cache.attend([1], q))
+    count = torch.arange(cfg.rows, dtype=torch.int32, device=dev()) % 3  # 0, 1 or 2 of the first tokens
+    keep = torch.where(count == 2, comp.b, count)
+    pos = torch.arange(comp.n_slots, dtype=torch.int32, device=dev())
+    row = torch.repeat_interleave(torch.arange(cfg.rows, device=dev()), comp.slot_off.diff())
+    cache.compact([0], [0], (pos - comp.slot_off[row]).to(torch.int32), comp.slot_off, keep)
+    assert cache.read_status() == 0 and torch.equal(cache.lens[:cfg.rows], keep)
+    k, v = torch.zeros_like(out[0])
+    cache.load([0], k, v, comp.slot_off)
+    held = (pos - comp.slot_off[row] < keep[row])[:, None]
+    assert torch.equal(k, torch.where(held, out[1][0], 0)) and torch.equal(v, torch.where(held, out[1][1], 0))
+
+
+def test_ragged_rows_that_stay_empty_and_that_span_pages():
+    """Appends over and over to rows of which some stay empty, some end in a page and some fill several."""
+    from tests import _paged as pg
+
+    rng = np.random.default_rng(3)
+    cache, m = pg.make(n_seqs=2, n_layers=2, heads=2, page=16, max_pages=20)
+    per_call = [0, 1, 15, 16, 17, 40, 0, 64]
+    for _ in range(4):
+        pg.fill(cache, m, per_call, rng)
+        m.check(cache)
+    assert 0 in m.len and max(len(x) for x in m.lists) == 16
+    assert any(n % 16 for n in m.len) and any(n and n % 16 == 0 for n in m.len)
