@@ -10,7 +10,6 @@
 // device wait, no atomics whose order shows: a page's count is an integer sum
 // and the bitmap a set. The plan is a chain of dependent loads and block sums
 // of one CTA, 2.5 us for 288 rows; what bounds the others stands at each.
-#include <atomic>
 #include <climits>
 
 #include "paged_common.cuh"
@@ -524,14 +523,6 @@ __device__ __forceinline__ void group_ends(const uint4* part, int q, int dq, flo
       m[n] = __uint_as_float((v[n] & 0xffff0000u) ^ 0x80000000u);
     }
   }
-}
-
-// (x & mask) | bits in one instruction: it takes one constant, so the other comes in a register.
-template <uint32_t MASK>
-__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t bits) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "n"(MASK), "r"(bits));
-  return r;
 }
 
 // Writes the 8 channels of codes w as m + c s, rounded once, with 16-byte
@@ -1104,40 +1095,12 @@ bool make_rows(const kv_paged_shape& sh, const int32_t* seq, int32_t n, int laye
   return true;
 }
 
-// Launch whose set-up overlaps the previous kernel's tail. Every kernel here waits for that kernel before it touches
-// memory, and reads with plain loads (the read-only path may not see what a kernel that was still running wrote).
-template <class... P, class... A>
-int launch_smem(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, k, P(args)...));
-}
-template <class... P, class... A>
-int launch(void (*k)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
-  return launch_smem(k, grid, threads, 0, st, args...);
-}
-
 template <int D, int QG, bool F32>
 int store_with(int blocks, const StoreArgs& a, cudaStream_t st) {
   using S = StoreSmem<D, QG, F32>;
   auto k = paged_store_kernel<D, QG, F32>;
-  static std::atomic<unsigned long long> ready{0};  // devices on which the kernel may take its shared memory
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return KV_ERR_CUDA;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
-      return KV_ERR_CUDA;
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
+  static std::atomic<unsigned long long> ready{0};
+  if (const int rc = allow_smem(k, S::kBytes, ready)) return rc;
   const int cap = (F32 ? 1 : 2) * sm_count();  // all resident
   return launch_smem(k, blocks < cap ? blocks : cap, kMoveWarps * 32, S::kBytes, st, a);
 }

@@ -47,7 +47,6 @@
 // order.
 #include <cuda_fp16.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "paged_common.cuh"
@@ -69,7 +68,7 @@ constexpr float kGrow = 8.f;  // the running maximum moves when a logit passes i
 
 // Shared memory of a CTA: the ring of stages, the warps' outputs and (maximum,
 // sum) on leaving a row, the rows' costs before them and lengths, two rows'
-// queries (matrix fragments; per query its sums by group and its unit).
+// queries (matrix fragments; per query its sums by group).
 template <int D, int NG, int NT, bool F32>
 struct Smem {
   static constexpr int kStages = D == 64 ? 4 : 2;  // as many as leave room for three CTAs an SM
@@ -130,13 +129,6 @@ __device__ __forceinline__ uint32_t add2_f16(uint32_t x, uint32_t y) {
   return r;
 }
 
-// (x & mask) | bits in one instruction: it takes one constant, so the other comes in a register.
-template <uint32_t MASK>
-__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t bits) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "n"(MASK), "r"(bits));
-  return r;
-}
 // The four nibble pairs of x (bits 4 n and 16 + 4 n) as two numbers c - 8 each, exactly: bf16, or (F16) fp16.
 struct CodeConst {
   uint32_t k7, s7;            // bf16: 128, which a code or-ed into makes 128 + c, and -136, in both halves
@@ -385,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
           ++it;  // this tile's copy is under way
           break;
         }
-        // scaled by a power of two each, as fragments, with their sums by group and units
+        // as fragments, with their sums by group
         {
           uint4* frag = reinterpret_cast<uint4*>(smem + S::kQ + (k & 1) * S::kQBytes);
           float* meta = reinterpret_cast<float*>(smem + S::kQ + (k & 1) * S::kQBytes + S::kFrag);
@@ -996,34 +988,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
   }
 }
 
-template <class K, class... A>
-int launch_pdl(K k, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, k, args...));
-}
-
 template <int D, int NG, int NT, bool F32>
 int run(AttnArgs a, cudaStream_t st) {
   using S = Smem<D, NG, NT, F32>;
   auto k = paged_attn_kernel<D, NG, NT, F32>;
-  static std::atomic<unsigned long long> ready{0};  // devices on which the kernel may take its shared memory
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return KV_ERR_CUDA;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess)
-      return KV_ERR_CUDA;
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
+  static std::atomic<unsigned long long> ready{0};
+  if (const int rc = allow_smem(k, S::kBytes, ready)) return rc;
   const int chunks = (a.R + S::NQ - 1) / S::NQ;
   const int per_sm = NT == 1 && !F32 ? kAttnCtasPerSm : 2;
   const int grid = max(1, sm_count() * per_sm / chunks);
@@ -1031,7 +1001,7 @@ int run(AttnArgs a, cudaStream_t st) {
   for (int r0 = 0; r0 < all; r0 += kAttnRows) {
     a.row0 = r0;
     a.n_rows = min(kAttnRows, all - r0);
-    const int rc = launch_pdl(k, dim3(grid, chunks), kThreads, S::kBytes, st, a);
+    const int rc = launch_smem(k, dim3(grid, chunks), kThreads, S::kBytes, st, a);
     if (rc) return rc;
   }
   return KV_OK;
