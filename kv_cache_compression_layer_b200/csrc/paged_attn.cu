@@ -2,11 +2,13 @@
 // cache (formats in include/kvcomp_paged.h).
 //
 // What bounds it: the codes and scales are read once, d + 8 G bytes a token
-// (144 at d = 128 and groups of 64), and 16 keys cost some 370 instructions, 128 of
-// them to unpack the codes, most on the logic pipe, which takes one every other
-// cycle. 192 rows of 6400 keys (g = 8): 54.3 us, 3.3 TB/s (a form that let terms
-// be cut at 2^-15 of the largest took 49). fp32: 77 us; 16 queries: 83; groups of
-// 32: 68; d = 64: 34.5; one row of one key: 5.9 us.
+// (144 at d = 128 and groups of 64), and 16 keys cost 370 instructions, 128 of
+// them to unpack the codes. Neither is at its limit (DRAM at 0.4, issue and the
+// logic pipe at 0.5): twelve attending warps an SM, each a chain of loads, unpacking,
+// products, exponentials and products again, leave its latencies in the open. 192
+// rows of 6400 keys (g = 8): 55.1 us, 3.2 TB/s (a form that let terms be cut at
+// 2^-15 of the largest took 49). fp32: 77 us; 16 queries: 85; groups of 32: 65; d =
+// 64: 35; one row of one key: 5.5 us.
 //
 // Products. With a group's step s and base m taken out of the sums,
 //   q.k = sum_g s_g (q.c)_g + m_g (sum of q over g),
@@ -15,17 +17,17 @@
 // with a shift and a logic instruction, c - 8 with one addition more (the bases
 // then count m - 128 s or m + 8 s).
 // Logits: bf16 queries are taken as they are times 128 + c, whose sums' last bits
-// are 2^-23 of 143 sum |q| at most; centred codes took 192 rows of 6400 keys from
-// 54.8 to 58.8 us. fp32 queries are three bf16 each (24 bits) times c - 8.
+// are 2^-23 of 143 sum |q| at most; with centred codes 192 rows of 6400 keys took
+// 58.8 us against 54.8. fp32 queries are three bf16 each (24 bits) times c - 8.
 // Outputs: p' is rounded to fp16 (2^-11 of a term) times c - 8 in fp16 (or-ed into
-// 0x6400 a code is 1024 + c, into 0x5400 64 + c), under a scale for each group of
-// channels, a power of two that a row's first keys choose. fp16 reaches from 2^-24
-// to 2^16, so this holds while steps stay within 2^10 of each other; before the
-// first keys whose steps do not (each lane looks at one key's), the row's sums
-// drop their scales, and from there on p' is two bf16 (16 bits), which need none.
-// So it is for a row's last keys too, and for fp32 with three bf16, always: no
-// group, token or query costs another its bits. Two bf16 for all keys took 59.5
-// us, a scale for each query and group that follows its largest p' 60.5.
+// 0x6400 a code is 1024 + c, into 0x5400 64 + c), under a scale, a power of two
+// that a row's first keys choose. fp16 reaches from 2^-24 to 2^16, so this holds
+// while steps stay within 2^10 of each other; before the first tile of which they
+// do not (each lane looks at one key's), the row's sums drop the scale, and from
+// there on p' is two bf16 (16 bits), which need none. So it is for a row's last
+// keys too, and for fp32 with three bf16, always: no group, token or query costs
+// another its bits. Two bf16 for all keys took 59.5 us, a scale for each query and
+// group that follows its largest p' 60.5; rows that leave fp16 take 64.
 // Both products have the cache as the 16-row operand (mma.sync m16n8k16: keys x
 // queries, then channels x queries), so up to 8 queries cost no padding; a
 // warp's fragments are one 16-byte load of K codes a key and 8-byte loads of V
@@ -534,11 +536,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       m2[nt][0] = m2[nt][1] = thr[nt][0] = thr[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    float om[NG];         // the scales of p' and O by group of channels; 0: not yet chosen
-    bool wide = F32;      // no scale any more: steps lay too far apart
-    bool moved = false;   // sums lie in the warp's part of obuf
-#pragma unroll
-    for (int z = 0; z < NG; ++z) om[z] = F32 ? 1.f : 0.f;
+    float om = F32 ? 1.f : 0.f;  // the scale of p' and O; 0: not yet chosen
+    bool wide = F32;             // no scale any more: steps lay too far apart
+    bool moved = false;          // sums lie in the warp's part of obuf
     // This lane's four channels of part h of a row and query (nt, x) there.
     auto spot = [&](int nt, int x, int h) {
       return reinterpret_cast<float4*>(obuf + (warp * NQ + nt * 8 + 2 * tig + x) * S::kORow + 32 * h + 4 * grp);
@@ -627,13 +627,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       // ---- softmax: the running maximum follows only when a logit passes it by far
       bool grow = false, odd = false;
       if constexpr (!F32) {
-        if (!wide) {  // this lane's key's steps
-          const int at = warp * 16 + (lane & 15) + 64 * (U == 2 ? lane >> 4 : u0);
+        if (!wide && u0 == 0) {  // the steps of the warp's 32 keys of the tile, a key a lane
+          const int at = warp * 16 + (lane & 15) + 64 * (lane >> 4);
           uint32_t sw[NG];
           load_scales<NG>(st + S::kVs + at * (NG * 4), sw);
 #pragma unroll
           for (int z = 0; z < NG; ++z) {
-            const float x = lo_f(sw[z]) * om[z];
+            const float x = lo_f(sw[z]) * om;
             odd |= !(x >= kReachLo && x <= kReachHi);
           }
           if (MASKED) odd &= t * kTile + at < len;
@@ -649,43 +649,36 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
       if (__any_sync(0xffffffffu, grow)) {
         if constexpr (!F32) {
           if (__any_sync(0xffffffffu, odd)) {
-            // the row's first keys choose the scales; steps that are out of reach end them
-            const bool first = om[0] == 0.f;
-            bool out = !first;
-#pragma unroll
-            for (int z = 0; z < NG; ++z) {
-              float top = 0.f, low = INFINITY;
-#pragma unroll
-              for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  if (MASKED && key0 + 64 * u + 8 * x >= len) continue;
-                  const float sc = lo_f(vs[u][x][z]);
-                  top = fmaxf(top, sc);
-                  low = sc >= 0.f ? fminf(low, sc) : 0.f;  // NaN: no reach
-                }
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-              }
-              const float choice = pow2(4 - min(100, max(-96, (int)(__float_as_uint(top) >> 23) - 127)));
-              out |= !(top * choice <= kReachHi && low * choice >= kReachLo);
-              if (first) om[z] = choice;
-            }
-            if (out) {
-              wide = true;
+            // the row's first keys choose the scale; steps that are out of its reach end it
+            float top = 0.f, low = INFINITY;
+            const int at = warp * 16 + (lane & 15) + 64 * (lane >> 4);
+            if (t * kTile + at < len) {
+              uint32_t sw[NG];
+              load_scales<NG>(st + S::kVs + at * (NG * 4), sw);
 #pragma unroll
               for (int z = 0; z < NG; ++z) {
-                const float inv = __frcp_rn(om[z]);
-                om[z] = 1.f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int h = 2 * z * W / NG; h < 2 * (z + 1) * W / NG; ++h)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) O[nt][h][x] *= inv;
+                const float sc = lo_f(sw[z]);
+                top = fmaxf(top, sc);
+                low = sc >= 0.f ? fminf(low, sc) : 0.f;  // NaN: out of reach
               }
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+            }
+            const bool first = om == 0.f;
+            if (first) om = pow2(4 - min(100, max(-96, (int)(__float_as_uint(top) >> 23) - 127)));
+            if (!first || !(top * om <= kReachHi && low * om >= kReachLo)) {
+              wide = true;
+              const float inv = __frcp_rn(om);
+              om = 1.f;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2 * W; ++h)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) O[nt][h][x] *= inv;
               if (!WIDE) return false;
             }
           }
@@ -724,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         uint32_t b[NT][NG][PP][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
+          float p[4], po[4];
           bool seen[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -732,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
             p[x] = ex2_approx(fmaf(y[u][nt][x], a.scale2, -m2[nt][x & 1]));
             if (!seen[x]) p[x] = 0.f;
             l[nt][x & 1] += p[x];
+            po[x] = F32 ? p[x] : p[x] * om;
           }
 #pragma unroll
           for (int z = 0; z < NG; ++z) {
@@ -739,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const float sc = lo_f(vs[u][x >> 1][z]), ba = fmaf(8.f, sc, hi_f(vs[u][x >> 1][z]));
-              ps[x] = p[x] * (F32 ? sc : sc * om[z]);
+              ps[x] = po[x] * sc;
               if constexpr (MASKED) {
                 off[nt][z][x & 1] += seen[x] ? p[x] * ba : 0.f;  // a token that another query sees may be NaN
                 if (!seen[x]) ps[x] = 0.f;
@@ -811,20 +805,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
         // 6400 keys, g = 16, 82 us against 74 when measured; 8 queries with groups of 32, 60.7 against 58; 8 with groups
         // of 64, 49.8 against 53.5 one after the other)
         constexpr int U = NT == 1 && (NG < 4 || F32) ? 2 : 1;
-        int u0 = 0;
-        bool fast = tok + 64 + 16 <= lim_min && (F32 || !wide);
-        if (fast) {
-#pragma unroll 1
-          for (int u = 0; u < 2; u += U)
-            if (!attend(std::integral_constant<int, U>{}, std::false_type{}, stage, u, t)) {
-              fast = false;
-              u0 = u;
-              break;
-            }
+        bool done = false;
+        if (tok + 64 + 16 <= lim_min && (F32 || !wide)) {
+          done = attend(std::integral_constant<int, U>{}, std::false_type{}, stage, 0, t);
+          if (U == 1 && done) attend(std::integral_constant<int, U>{}, std::false_type{}, stage, 1, t);
         }
-        if (!fast) {
+        if (!done) {
 #pragma unroll 1
-          for (int u = u0; u < 2 && tok + 64 * u < len; ++u)
+          for (int u = 0; u < 2 && tok + 64 * u < len; ++u)
             attend(std::integral_constant<int, 1>{}, std::true_type{}, stage, u, t);
         }
         __syncwarp();
@@ -834,13 +822,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !F32 ? kAttnCtasPerSm : 2
           ++turn;
         }
       }
+      const float inv = om > 0.f ? __frcp_rn(om) : 0.f;  // 0: the warp had no key
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int h = 0; h < W; ++h) {
-            const float inv = om[h * NG / W] > 0.f ? __frcp_rn(om[h * NG / W]) : 0.f;  // 0: the warp had no key
             float4 v = moved ? *spot(nt, x, h) : make_float4(0.f, 0.f, 0.f, 0.f);
             v.x = fmaf(O[nt][2 * h][x], inv, v.x);
             v.y = fmaf(O[nt][2 * h][2 + x], inv, v.y);
